@@ -26,6 +26,8 @@ H2O_POLICY_NORMALIZED = 1
 H2O_POLICY_INSERT_ALWAYS = 2
 H2O_BF16 = 0
 H2O_FP32 = 1
+H2O_TREE_MAX_T = 256
+H2O_CKPT_GROUP = 32
 
 STATUS_NAMES = {0: "H2O_OK", -1: "H2O_ERR_ARG", -2: "H2O_ERR_ALIGN", -3: "H2O_ERR_OOM",
                 -4: "H2O_ERR_CUDA", -5: "H2O_ERR_TIMEOUT", -6: "H2O_ERR_POISONED",
@@ -35,6 +37,7 @@ STATUS_NAMES = {0: "H2O_OK", -1: "H2O_ERR_ARG", -2: "H2O_ERR_ALIGN", -3: "H2O_ER
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
+_Z = ctypes.c_size_t
 SIGNATURES = [
     ("h2o_create", _I, [_I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
     ("h2o_create_ex", _I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
@@ -63,6 +66,12 @@ SIGNATURES = [
     ("h2o_version", ctypes.c_char_p, []),
     ("h2o_kernel_plan", _I, [_P, _I, ctypes.POINTER(ctypes.c_char_p), _I]),
     ("h2o_select_noalloc", _I, [_I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    ("h2o_tree_attend", _I, [_P, _P, _P, _P, _P, _P, _P, _I, _P]),
+    ("h2o_checkpoint_bytes", _I, [_P, _I, _I, ctypes.POINTER(_Z)]),
+    ("h2o_checkpoint_save", _I, [_P, _P, _P, _P, _I, _P, _Z, _P]),
+    ("h2o_checkpoint_restore", _I, [_P, _P, _Z, _I, _I, _P, _P, _P, _P, _P, _P]),
+    ("h2o_checkpoint_backward", _I, [_P, _P, _Z, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    ("h2o_carry_grad", _I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     ("h2o_profile_begin", _I, [_P, _I]),
     ("h2o_profile_end", _I, [_P, _I, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
                              ctypes.POINTER(_I)]),

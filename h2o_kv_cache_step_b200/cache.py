@@ -5,6 +5,7 @@ current CUDA stream; every computation happens in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -22,6 +23,44 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
 
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
+
+
+class H2OCheckpoint:
+    """A step's inputs in 8 bits: the device record ``H2OCache.checkpoint``
+    writes, with the sizes it was written for. ``buffer`` (uint8) holds the
+    codes of q, k, v and of the ``n`` valid slots of K and V, then their scales
+    in the same order (one per 32 channels)."""
+
+    def __init__(self, buffer: torch.Tensor, B: int, Hq: int, Hkv: int, d: int, T: int, n: int):
+        rows = B * (Hq * T + 2 * Hkv * T + 2 * Hkv * n)
+        if (buffer.dtype != torch.uint8 or not buffer.is_cuda or buffer.dim() != 1 or not buffer.is_contiguous()
+                or buffer.numel() != rows * (d + d // _lib.H2O_CKPT_GROUP * 4)):
+            raise ValueError(f"buffer: need a flat contiguous CUDA uint8 tensor of "
+                             f"{rows * (d + d // _lib.H2O_CKPT_GROUP * 4)} bytes, got {buffer.dtype} "
+                             f"{tuple(buffer.shape)}")
+        self.buffer, self.T, self.n = buffer, T, n
+        self.shape = (B, Hq, Hkv, d)
+
+    @property
+    def nbytes(self) -> int:
+        return self.buffer.numel()
+
+    def _split(self, flat: torch.Tensor, per_row: int):
+        B, Hq, Hkv, _ = self.shape
+        shapes = [(B, Hq, self.T), (B, Hkv, self.T), (B, Hkv, self.T), (B, Hkv, self.n), (B, Hkv, self.n)]
+        sizes = [x[0] * x[1] * x[2] * per_row for x in shapes]
+        return tuple(p.view(*x, per_row) for p, x in zip(flat.split(sizes), shapes))
+
+    def _codes_end(self) -> int:
+        return self.nbytes // (_lib.H2O_CKPT_GROUP + 4) * _lib.H2O_CKPT_GROUP
+
+    def codes(self):
+        """int8 views of the codes of (q, k, v, K, V)."""
+        return self._split(self.buffer[: self._codes_end()].view(torch.int8), self.shape[3])
+
+    def scales(self):
+        """float32 views of their scales, [.., d / 32]."""
+        return self._split(self.buffer[self._codes_end():].view(torch.float32), self.shape[3] // _lib.H2O_CKPT_GROUP)
 
 
 class H2OCache:
@@ -122,6 +161,119 @@ class H2OCache:
         self._check(lib().h2o_backward(self._h, _ptr(q), _ptr(k), _ptr(v), _ptr(lse), _ptr(dout), T,
                                        _ptr(dq), _ptr(dK), _ptr(dV), _ptr(dk), _ptr(dv), _stream_ptr(stream)))
         return dq, dK, dV, dk, dv
+
+    # -- operators next to the step -----------------------------------------
+    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> ctypes.c_void_p:
+        if t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return _ptr(t)
+
+    def _on(self, stream, *used):
+        """The stream of a call, its pointer, and its inputs marked as used there
+        where it is not the current one."""
+        cur = torch.cuda.current_stream(self.device)
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream: on {stream.device}, the cache is on {self.device}")
+        if stream is None or stream == cur:
+            return None, ctypes.c_void_p(cur.cuda_stream)
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+        return stream, ctypes.c_void_p(stream.cuda_stream)
+
+    def _empty(self, stream, dtype: torch.dtype, *shapes):
+        """New tensors that belong to the stream of the call."""
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            return [torch.empty(x, dtype=dtype, device=self.device) for x in shapes]
+
+    def tree_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent: torch.Tensor, stream=None):
+        """Attention of a tree of T drafted tokens per sequence over the cache,
+        which stays as it is. q [B,Hq,T,d], k and v [B,Hkv,T,d], parent int32
+        [B,T]: -1 for a child of the committed sequence, an earlier node's index,
+        or any other value for an absent node. Returns (out [B,Hq,T,d], lse
+        float32 [B,Hq,T]); absent rows hold 0 and -inf. Commit the accepted path
+        with step()."""
+        if q.dim() != 4:
+            raise ValueError("q: need [B, Hq, T, d]")
+        B, T = self.B, q.shape[2]
+        args = [self._need("q", q, self.dtype, B, self.Hq, T, self.d),
+                self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
+                self._need("v", v, self.dtype, B, self.Hkv, T, self.d),
+                self._need("parent", parent, torch.int32, B, T)]
+        s, sp = self._on(stream, q, k, v, parent)
+        (out,) = self._empty(s, self.dtype, (B, self.Hq, T, self.d))
+        (lse,) = self._empty(s, torch.float32, (B, self.Hq, T))
+        self._check(lib().h2o_tree_attend(self._h, *args, _ptr(out), _ptr(lse), T, sp))
+        return out, lse
+
+    def checkpoint(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> H2OCheckpoint:
+        """The inputs of the step that is about to run, in 8 bits: the chunk and
+        the valid slots of the current cache."""
+        if q.dim() != 4:
+            raise ValueError("q: need [B, Hq, T, d]")
+        B, T, n = self.B, q.shape[2], self.counters()[1]
+        args = [self._need("q", q, self.dtype, B, self.Hq, T, self.d),
+                self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
+                self._need("v", v, self.dtype, B, self.Hkv, T, self.d)]
+        bytes_ = ctypes.c_size_t()
+        self._check(lib().h2o_checkpoint_bytes(self._h, T, n, ctypes.byref(bytes_)))
+        s, sp = self._on(stream, q, k, v)
+        (buf,) = self._empty(s, torch.uint8, (bytes_.value,))
+        self._check(lib().h2o_checkpoint_save(self._h, *args, T, _ptr(buf), bytes_, sp))
+        return H2OCheckpoint(buf, B, self.Hq, self.Hkv, self.d, T, n)
+
+    def _record(self, ck: H2OCheckpoint):
+        if ck.shape != (self.B, self.Hq, self.Hkv, self.d) or ck.buffer.device != self.device:
+            raise ValueError(f"checkpoint: of {ck.shape} on {ck.buffer.device}, the cache is "
+                             f"{(self.B, self.Hq, self.Hkv, self.d)} on {self.device}")
+        return _ptr(ck.buffer), ck.nbytes, ck.T, ck.n
+
+    def checkpoint_restore(self, ck: H2OCheckpoint, stream=None):
+        """The values a checkpoint stands for: (q, k, v, K, V), K and V over all
+        C slots with zeros in the empty ones. The cache itself is not changed."""
+        rec = self._record(ck)
+        s, sp = self._on(stream, ck.buffer)
+        q, k, v, K, V = self._empty(s, self.dtype, (self.B, self.Hq, ck.T, self.d),
+                                    *[(self.B, self.Hkv, x, self.d) for x in (ck.T, ck.T, self.C, self.C)])
+        self._check(lib().h2o_checkpoint_restore(self._h, *rec, _ptr(q), _ptr(k), _ptr(v), _ptr(K), _ptr(V), sp))
+        return q, k, v, K, V
+
+    def checkpoint_backward(self, ck: H2OCheckpoint, dout: torch.Tensor, stream=None):
+        """Gradients of the checkpointed step's attention at the values the
+        checkpoint stands for: (dq, dK, dV, dk, dv) in the cache's type, dK and
+        dV over the C slots. The cache itself is not read."""
+        rec = self._record(ck)
+        do = self._need("dout", dout, self.dtype, self.B, self.Hq, ck.T, self.d)
+        s, sp = self._on(stream, ck.buffer, dout)
+        g = self._empty(s, self.dtype, (self.B, self.Hq, ck.T, self.d),
+                        *[(self.B, self.Hkv, x, self.d) for x in (self.C, self.C, ck.T, ck.T)])
+        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, *[_ptr(t) for t in g], sp))
+        return tuple(g)
+
+    def carry_grad(self, token_slots: torch.Tensor, n: int, dK: torch.Tensor, dV: torch.Tensor, dk: torch.Tensor,
+                   dv: torch.Tensor, gK_next: torch.Tensor | None = None, gV_next: torch.Tensor | None = None,
+                   stream=None):
+        """The gradient of the cache after a step (gK_next, gV_next: float32
+        [B,Hkv,C,d], None after the last step) handed back through its eviction.
+        token_slots: int32 [B,Hkv,T], as token_slots() returned after the step;
+        n: the valid slots before it; dK, dV, dk, dv: its own gradients. Returns
+        (gK, gV, gk, gv): float32 gradients of the cache before the step, and
+        the chunk's whole gradients in the cache's type."""
+        if token_slots.dim() != 3:
+            raise ValueError("token_slots: need [B, Hkv, T]")
+        T = token_slots.shape[2]
+        cache, chunk = (self.B, self.Hkv, self.C, self.d), (self.B, self.Hkv, T, self.d)
+        args = [self._need("token_slots", token_slots, torch.int32, self.B, self.Hkv, T), T, int(n),
+                self._need("dK", dK, self.dtype, *cache), self._need("dV", dV, self.dtype, *cache),
+                self._need("dk", dk, self.dtype, *chunk), self._need("dv", dv, self.dtype, *chunk)]
+        for name, t in (("gK_next", gK_next), ("gV_next", gV_next)):
+            args.append(None if t is None else self._need(name, t, torch.float32, *cache))
+        s, sp = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
+        gK, gV = self._empty(s, torch.float32, cache, cache)
+        gk, gv = self._empty(s, self.dtype, chunk, chunk)
+        self._check(lib().h2o_carry_grad(self._h, *args, _ptr(gK), _ptr(gV), _ptr(gk), _ptr(gv), sp))
+        return gK, gV, gk, gv
 
     def set_policy(self, policy: int) -> None:
         """Eviction ranking for the following steps: _lib.H2O_POLICY_SUM (the
@@ -249,4 +401,4 @@ class H2OCache:
         return [names[i].decode() for i in range(k)]
 
 
-__all__ = ["H2OCache", "_lib"]
+__all__ = ["H2OCache", "H2OCheckpoint", "_lib"]

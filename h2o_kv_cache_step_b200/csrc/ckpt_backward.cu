@@ -1,0 +1,265 @@
+// ckpt_backward.cu -- backward of a step's attention at the values an 8-bit
+// checkpoint stands for, on the CUDA cores (fp32 contexts; fp32 arithmetic).
+//
+// Row i of a head sees the n cache slots and the chunk tokens t <= i. With
+//   s_ij = q_i . k_j / sqrt(d),  p_ij = exp(s_ij) / sum_j exp(s_ij),
+//   dp_ij = dO_i . v_j,          D_i = sum_j p_ij dp_ij,
+//   ds_ij = p_ij (dp_ij - D_i):
+//   dq_i = sum_j ds_ij k_j / sqrt(d), dk_j = sum_i ds_ij q_i / sqrt(d),
+//   dv_j = sum_i p_ij dO_i,
+// sums over i running over every query head of the key's KV head. The softmax
+// statistics are recomputed: the restored keys are not the ones the forward
+// saw, so its log-sum-exp would not normalise these weights.
+#include <math.h>
+
+#include "operators.h"
+#include "vec.cuh"
+
+namespace h2o {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kRows = 2;  // dq: query rows per CTA, in registers
+constexpr int kKeys = 2;  // dk, dv: keys per CTA, in registers
+
+__device__ __forceinline__ float sum8(float x) {  // over the eight lanes of a key or row
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    return x + __shfl_xor_sync(0xffffffffu, x, 4);
+}
+__device__ __forceinline__ float sum_subs(float x) {  // over a warp's four lane groups
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+__device__ __forceinline__ float4 sum_subs(float4 a) {
+    return make_float4(sum_subs(a.x), sum_subs(a.y), sum_subs(a.z), sum_subs(a.w));
+}
+
+// dq of kRows rows of one KV group (row = head-in-group * T + i), and their
+// statistics. One pass over the keys with a running maximum, keeping
+// A = sum e dp k, Z = sum e k, sum e dp and sum e (e = exp(s - max)):
+// dq = (A - D Z) / (sum e sqrt(d)). Eight lanes share a key.
+template <typename E, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
+                    const E* __restrict__ V, const E* __restrict__ dout, E* __restrict__ dq, float4* __restrict__ stats,
+                    int G, int T, int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+    constexpr int Q4 = D / 32;
+    __shared__ float4 part[2][kWarps][kRows][D / 4];
+    __shared__ float part_s[kWarps][kRows][3];  // maximum, sum e, sum e dp
+    const int R = G * T;
+    const size_t bg = blockIdx.x / blocks_per_group;
+    const int r0 = (blockIdx.x % blocks_per_group) * kRows;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane >> 3, l8 = lane & 7;
+    const size_t row0 = bg * R + r0;
+    float4 qr[kRows][Q4], dr[kRows][Q4], A[kRows][Q4], Z[kRows][Q4];
+    float m[kRows], l[kRows], w[kRows];
+    int tok[kRows], last = 0;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int rr = min(r0 + r, R - 1);
+        tok[r] = rr % T;
+        last = max(last, tok[r]);
+        m[r] = -INFINITY;
+        l[r] = w[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            qr[r][c] = load4(q + (bg * R + rr) * D + 32 * c + 4 * l8);
+            dr[r][c] = load4(dout + (bg * R + rr) * D + 32 * c + 4 * l8);
+            A[r][c] = Z[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    const int total = n + last + 1;
+    for (int u0 = warp * 4; u0 < total; u0 += kWarps * 4) {
+        const int u = u0 + sub;
+        const int uu = min(u, total - 1);
+        const E* kp = uu < n ? K + (bg * pitch + uu) * D : k + (bg * T + (uu - n)) * D;
+        const E* vp = uu < n ? V + (bg * pitch + uu) * D : v + (bg * T + (uu - n)) * D;
+        float4 kk[Q4], vv[Q4];
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) kk[c] = load4(kp + 32 * c + 4 * l8);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) vv[c] = load4(vp + 32 * c + 4 * l8);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float s = 0.f, dp = 0.f;
+#pragma unroll
+            for (int c = 0; c < Q4; ++c) {
+                s = dot4(qr[r][c], kk[c], s);
+                dp = dot4(dr[r][c], vv[c], dp);
+            }
+            s = sum8(s) * scale_log2;
+            dp = sum8(dp);
+            if (u < total && u - n <= tok[r]) {
+                const float mn = fmaxf(m[r], s);
+                const float a = exp2f(m[r] - mn), e = exp2f(s - mn), ed = e * dp;
+                l[r] = fmaf(l[r], a, e);
+                w[r] = fmaf(w[r], a, ed);
+                m[r] = mn;
+#pragma unroll
+                for (int c = 0; c < Q4; ++c) {
+                    A[r][c] = fma4(ed, kk[c], scale4(A[r][c], a));
+                    Z[r][c] = fma4(e, kk[c], scale4(Z[r][c], a));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        float M = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8));
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+        const float f = m[r] == -INFINITY ? 0.f : exp2f(m[r] - M);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            const float4 a = sum_subs(scale4(A[r][c], f)), z = sum_subs(scale4(Z[r][c], f));
+            if (sub == 0) {
+                part[0][warp][r][8 * c + l8] = a;
+                part[1][warp][r][8 * c + l8] = z;
+            }
+        }
+        const float ls = sum_subs(l[r] * f), ws = sum_subs(w[r] * f);
+        if (lane == 0) {
+            part_s[warp][r][0] = M;
+            part_s[warp][r][1] = ls;
+            part_s[warp][r][2] = ws;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRows * (D / 4); e += kWarps * 32) {
+        const int r = e / (D / 4), x = e % (D / 4);
+        if (r0 + r >= R) continue;
+        float M = -INFINITY, L = 0.f, W = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), z = a;
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, part_s[i][r][0]);
+        for (int i = 0; i < kWarps; ++i) {
+            const float f = part_s[i][r][0] == -INFINITY ? 0.f : exp2f(part_s[i][r][0] - M);
+            L = fmaf(part_s[i][r][1], f, L);
+            W = fmaf(part_s[i][r][2], f, W);
+            a = fma4(f, part[0][i][r][x], a);
+            z = fma4(f, part[1][i][r][x], z);
+        }
+        const float Dr = W / L, g = scale / L;
+        // D z is rounded on its own, so that a row that sees one key gets exactly zero
+        store4(dq + (row0 + r) * D + 4 * x,
+               make_float4((a.x - __fmul_rn(Dr, z.x)) * g, (a.y - __fmul_rn(Dr, z.y)) * g,
+                           (a.z - __fmul_rn(Dr, z.z)) * g, (a.w - __fmul_rn(Dr, z.w)) * g));
+        if (x == 0) stats[row0 + r] = make_float4(M, 1.f / L, Dr, 0.f);
+    }
+}
+
+// dk and dv of kKeys keys of one KV group: key u < C is cache slot u (zero
+// gradients from n on), u >= C is chunk token u - C. Eight lanes share a query
+// row, the CTA takes 32 rows at a time.
+template <typename E, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
+                      const E* __restrict__ V, const E* __restrict__ dout, const float4* __restrict__ stats,
+                      E* __restrict__ dK, E* __restrict__ dV, E* __restrict__ dk, E* __restrict__ dv, int G, int C, int T,
+                      int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+    constexpr int Q4 = D / 32;
+    __shared__ float4 part[2][kWarps][kKeys][D / 4];
+    const int R = G * T;
+    const size_t bg = blockIdx.x / blocks_per_group;
+    const int u0 = (blockIdx.x % blocks_per_group) * kKeys;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane >> 3, l8 = lane & 7;
+    float4 kr[kKeys][Q4], vr[kKeys][Q4], gk[kKeys][Q4], gv[kKeys][Q4];
+    int from[kKeys];  // first row token that sees the key (T: none)
+    int first = T;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+        const int u = u0 + j;
+        const bool cache = u < C;
+        from[j] = cache ? (u < n ? 0 : T) : (u < C + T ? u - C : T);
+        first = min(first, from[j]);
+        const E* kp = cache ? K + (bg * pitch + u) * D : k + (bg * T + (u - C)) * D;
+        const E* vp = cache ? V + (bg * pitch + u) * D : v + (bg * T + (u - C)) * D;
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            gk[j][c] = gv[j][c] = zero;
+            kr[j][c] = from[j] < T ? load4(kp + 32 * c + 4 * l8) : zero;
+            vr[j][c] = from[j] < T ? load4(vp + 32 * c + 4 * l8) : zero;
+        }
+    }
+    const int span = T - first;  // rows of each head from `first` on
+    for (int x0 = warp * 4; x0 < G * span; x0 += kWarps * 4) {
+        const int x = min(x0 + sub, G * span - 1);
+        const int i = first + x % span;
+        const size_t row = bg * R + (size_t)(x / span) * T + i;
+        const bool in = x0 + sub < G * span;
+        float4 qq[Q4], dd[Q4];
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) qq[c] = load4(q + row * D + 32 * c + 4 * l8);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) dd[c] = load4(dout + row * D + 32 * c + 4 * l8);
+        const float4 st = stats[row];
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j) {
+            float s = 0.f, dp = 0.f;
+#pragma unroll
+            for (int c = 0; c < Q4; ++c) {
+                s = dot4(qq[c], kr[j][c], s);
+                dp = dot4(dd[c], vr[j][c], dp);
+            }
+            s = sum8(s) * scale_log2;
+            dp = sum8(dp);
+            if (in && i >= from[j]) {
+                const float p = exp2f(s - st.x) * st.y, ds = p * (dp - st.z);
+#pragma unroll
+                for (int c = 0; c < Q4; ++c) {
+                    gv[j][c] = fma4(p, dd[c], gv[j][c]);
+                    gk[j][c] = fma4(ds, qq[c], gk[j][c]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j)
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            const float4 a = sum_subs(gk[j][c]), b = sum_subs(gv[j][c]);
+            if (sub == 0) {
+                part[0][warp][j][8 * c + l8] = a;
+                part[1][warp][j][8 * c + l8] = b;
+            }
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kKeys * (D / 4); e += kWarps * 32) {
+        const int j = e / (D / 4), x = e % (D / 4), u = u0 + j;
+        if (u >= C + T) continue;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        for (int i = 0; i < kWarps; ++i) {
+            a = add4(a, part[0][i][j][x]);
+            b = add4(b, part[1][i][j][x]);
+        }
+        E* ka = u < C ? dK + (bg * C + u) * D : dk + (bg * T + (u - C)) * D;
+        E* va = u < C ? dV + (bg * C + u) * D : dv + (bg * T + (u - C)) * D;
+        store4(ka + 4 * x, scale4(a, scale));
+        store4(va + 4 * x, b);
+    }
+}
+
+template <typename E, int D>
+cudaError_t backward_typed(const CkptBwdArgs& a) {
+    const float scale = 1.f / sqrtf((float)D), scale_log2 = kLog2e * scale;
+    const int G = a.Hq / a.Hkv, groups = a.B * a.Hkv;
+    const int rows = (G * a.T + kRows - 1) / kRows, keys = (a.C + a.T + kKeys - 1) / kKeys;
+    ckpt_dq_simt_kernel<E, D><<<groups * rows, kWarps * 32, 0, a.stream>>>(
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq, a.stats, G,
+        a.T, a.n, a.pitch, rows, scale_log2, scale);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ckpt_dkdv_simt_kernel<E, D><<<groups * keys, kWarps * 32, 0, a.stream>>>(
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, a.stats, (E*)a.dK,
+        (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n, a.pitch, keys, scale_log2, scale);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a) {
+    if (a.dtype == 1) return a.d == 64 ? backward_typed<float, 64>(a) : backward_typed<float, 128>(a);
+    return a.d == 64 ? backward_typed<__nv_bfloat16, 64>(a) : backward_typed<__nv_bfloat16, 128>(a);
+}
+
+}  // namespace h2o

@@ -1,0 +1,165 @@
+// tree.cu -- attention of a tree of drafted tokens over the cache, on the CUDA
+// cores (fp32 contexts; the arithmetic is fp32 for either element type).
+//
+// Row i of sequence b sees the n valid cache slots and the nodes on its path to
+// the root, itself included:
+//   O_i = sum_j p_ij v_j,  p_ij = exp(s_ij - LSE_i),  s_ij = q_i . k_j / sqrt(d),
+//   LSE_i = log sum_j exp(s_ij).
+// A node whose path does not end in a root (parent -1) is absent: O = 0,
+// LSE = -inf.
+#include <math.h>
+
+#include "operators.h"
+#include "vec.cuh"
+
+namespace h2o {
+namespace {
+
+constexpr int kRows = 4;    // query rows per CTA, in registers
+constexpr int kWarps = 8;
+
+// One CTA per kRows query rows of one KV group (row = head-in-group * T + i).
+// Eight lanes share a key (d / 8 columns each), so a warp takes four keys and
+// the CTA 32 at a time, straight from global memory into registers; every lane
+// group keeps its own running maximum, sum and output, merged at the end.
+template <typename E, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
+                 const int32_t* __restrict__ parent, const E* __restrict__ Kc, const E* __restrict__ Vc,
+                 E* __restrict__ out, float* __restrict__ lse, int Hq, int Hkv, int C, int T, int n, int blocks_per_group,
+                 float scale_log2) {
+    constexpr int Q4 = D / 32;  // float4 per lane and row
+    __shared__ uint32_t mask[kRows][kTreeMaskWords];
+    __shared__ int present[kRows];
+    __shared__ float part[kWarps][kRows][D];
+    __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
+    const int G = Hq / Hkv, R = G * T;
+    const int bg = blockIdx.x / blocks_per_group, r0 = (blockIdx.x % blocks_per_group) * kRows;
+    const int b = bg / Hkv;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane >> 3, l8 = lane & 7;
+    const size_t row0 = (size_t)bg * R + r0;  // [B,Hq,T] rows of a group are contiguous
+
+    // the path of each row's node to the root: parents have smaller indices, so
+    // the walk ends
+    if (threadIdx.x < kRows) {
+        const int r = threadIdx.x;
+        for (int w = 0; w < kTreeMaskWords; ++w) mask[r][w] = 0;
+        int at = r0 + r < R ? (r0 + r) % T : -2;
+        while (at >= 0) {
+            mask[r][at >> 5] |= 1u << (at & 31);
+            const int up = parent[(size_t)b * T + at];
+            at = up == -1 ? -1 : (up >= 0 && up < at) ? up : -2;
+        }
+        present[r] = at == -1;
+    }
+    float4 qr[kRows][Q4], acc[kRows][Q4];
+    float m[kRows], l[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        const size_t row = row0 + min(r, R - 1 - r0);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            qr[r][c] = load4(q + row * D + 32 * c + 4 * l8);
+            acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __syncthreads();
+
+    const int total = n + T;
+    for (int u0 = warp * 4; u0 < total; u0 += kWarps * 4) {
+        const int u = u0 + sub;
+        const bool in = u < total;
+        const int uu = in ? u : total - 1;
+        const E* kp = uu < n ? Kc + ((size_t)bg * C + uu) * D : k + ((size_t)bg * T + (uu - n)) * D;
+        const E* vp = uu < n ? Vc + ((size_t)bg * C + uu) * D : v + ((size_t)bg * T + (uu - n)) * D;
+        float4 kk[Q4], vv[Q4];
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) kk[c] = load4(kp + 32 * c + 4 * l8);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) vv[c] = load4(vp + 32 * c + 4 * l8);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < Q4; ++c)
+                s = fmaf(qr[r][c].x, kk[c].x, fmaf(qr[r][c].y, kk[c].y, fmaf(qr[r][c].z, kk[c].z, fmaf(qr[r][c].w, kk[c].w, s))));
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            // a key the row does not see touches nothing, whatever it holds
+            const bool vis = in && (u < n || ((mask[r][(u - n) >> 5] >> ((u - n) & 31)) & 1u));
+            s *= scale_log2;
+            const float mn = fmaxf(m[r], s);
+            if (vis && !(s == mn && mn == -INFINITY)) {
+                const float a = exp2f(m[r] - mn), p = exp2f(s - mn);
+                l[r] = fmaf(l[r], a, p);
+                m[r] = mn;
+#pragma unroll
+                for (int c = 0; c < Q4; ++c) {
+                    acc[r][c].x = fmaf(p, vv[c].x, acc[r][c].x * a);
+                    acc[r][c].y = fmaf(p, vv[c].y, acc[r][c].y * a);
+                    acc[r][c].z = fmaf(p, vv[c].z, acc[r][c].z * a);
+                    acc[r][c].w = fmaf(p, vv[c].w, acc[r][c].w * a);
+                }
+            }
+        }
+    }
+    // merge the four lane groups of a warp, then the warps
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        float M = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8));
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+        const float w = m[r] == -INFINITY && l[r] == 0.f ? 0.f : exp2f(m[r] - M);
+        float L = l[r] * w;
+        L += __shfl_xor_sync(0xffffffffu, L, 8);
+        L += __shfl_xor_sync(0xffffffffu, L, 16);
+#pragma unroll
+        for (int c = 0; c < Q4; ++c) {
+            float x[4] = {acc[r][c].x * w, acc[r][c].y * w, acc[r][c].z * w, acc[r][c].w * w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] += __shfl_xor_sync(0xffffffffu, x[e], 8);
+                x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
+            }
+            if (sub == 0) *reinterpret_cast<float4*>(&part[warp][r][32 * c + 4 * l8]) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        if (lane == 0) {
+            part_m[warp][r] = M;
+            part_l[warp][r] = L;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRows * D; e += kWarps * 32) {
+        const int r = e / D, x = e % D;
+        if (r0 + r >= R) continue;
+        float M = -INFINITY, L = 0.f, o = 0.f;
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_m[w][r]);
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = part_m[w][r] == -INFINITY && part_l[w][r] == 0.f ? 0.f : exp2f(part_m[w][r] - M);
+            L = fmaf(part_l[w][r], f, L);
+            o = fmaf(part[w][r][x], f, o);
+        }
+        out[(row0 + r) * D + x] = from_f32<E>(present[r] ? o / L : 0.f);
+        if (x == 0) lse[row0 + r] = present[r] ? (M + log2f(L)) * kLn2 : -INFINITY;
+    }
+}
+
+template <typename E, int D>
+cudaError_t tree_simt_typed(const TreeArgs& a) {
+    const int R = a.Hq / a.Hkv * a.T, per = (R + kRows - 1) / kRows;
+    tree_simt_kernel<E, D><<<a.B * a.Hkv * per, kWarps * 32, 0, a.stream>>>(
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, a.parent, (const E*)a.Kc, (const E*)a.Vc, (E*)a.out, a.lse, a.Hq,
+        a.Hkv, a.C, a.T, a.n, per, kLog2e / sqrtf((float)D));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_simt(const TreeArgs& a) {
+    if (a.dtype == 1) return a.d == 64 ? tree_simt_typed<float, 64>(a) : tree_simt_typed<float, 128>(a);
+    return a.d == 64 ? tree_simt_typed<__nv_bfloat16, 64>(a) : tree_simt_typed<__nv_bfloat16, 128>(a);
+}
+
+}  // namespace h2o

@@ -204,6 +204,112 @@ int h2o_counters(const h2o_ctx *ctx, int64_t *P, int64_t *n);
  * failure of this thread that had no context, e.g. in h2o_create). */
 const char *h2o_last_error(const h2o_ctx *ctx);
 
+/* ---- tree attention (speculative decoding) ------------------------------ */
+
+/* Largest number of drafted nodes per sequence. */
+#define H2O_TREE_MAX_T 256
+
+/* Attention of a tree of T drafted tokens per sequence over the cache, which
+ * stays as it is: a serving loop verifies all drafted nodes in one pass and
+ * then commits the accepted path with h2o_step (whose rows see the same keys).
+ * parent (device int32 [B, T]) gives the tree: parent[i] = -1 makes node i a
+ * child of the committed sequence, 0 <= parent[i] < i of that node; with any
+ * other value node i is absent (padding, where a sequence has fewer nodes), and
+ * so is every node below an absent one. Row i of a present node attends to the
+ * n valid cache slots, to its ancestors and to itself, GQA and scale as in
+ * h2o_step:
+ *   out [B, Hq, T, d]    softmax(q k / sqrt(d)) v,
+ *   lse [B, Hq, T]       float: log-sum-exp of the row's scaled logits;
+ * an absent node's row gets out = 0 and lse = -inf. A key that a row does not
+ * see leaves the row alone whatever it holds (NaN and infinities included); a
+ * row that sees a drafted node whose v holds a NaN or an infinity is NaN
+ * throughout on the tensor-core path. Device pointers; layouts, element type
+ * and alignment as h2o_step (parent and lse: 4 bytes). T <= H2O_TREE_MAX_T
+ * (H2O_ERR_UNSUPPORTED otherwise, and under H2O_POLICY_INSERT_ALWAYS, where
+ * the number of accepted tokens decides which slots a row may see). The scores
+ * do not change: only committed tokens count. Asynchronous on `stream`. The
+ * first call allocates a workspace; a call captured into a graph needs one call
+ * before it, and replays with the n of its capture. The workspace belongs to
+ * the context: its calls and replays must not overlap on the GPU. The paper has
+ * no counterpart of this entry point. */
+int h2o_tree_attend(h2o_ctx *ctx, const void *q, const void *k, const void *v,
+                    const int32_t *parent, void *out, float *lse, int T, void *stream);
+
+/* ---- 8-bit step checkpoints (training) ----------------------------------- */
+
+/* Channels of a row that share one scale. */
+#define H2O_CKPT_GROUP 32
+
+/* Bytes of the record of a step with a chunk of T tokens and n valid slots
+ * (0 <= n <= C): B * (Hq T + 2 Hkv T + 2 Hkv n) rows of d codes (int8) and
+ * d / H2O_CKPT_GROUP scales (float). */
+int h2o_checkpoint_bytes(const h2o_ctx *ctx, int T, int n, size_t *bytes);
+
+/* Record a step's inputs in 8 bits before the step runs: the chunk q, k, v
+ * (device, layouts of h2o_step) and the n valid slots of the context's current
+ * cache K, V ("Learning how to Forget", paper page, section "Gradient
+ * Computation Strategy for Sparse Attention": the backward needs the cache each
+ * step saw, which the steps after it overwrite). ckpt (device, 16-byte aligned,
+ * `bytes` >= h2o_checkpoint_bytes of T and the current n) receives
+ *   int8   codes:  q [B,Hq,T,d], k [B,Hkv,T,d], v [B,Hkv,T,d],
+ *                  K [B,Hkv,n,d], V [B,Hkv,n,d], one after the other,
+ *   float  scales: the same order, [.., d / H2O_CKPT_GROUP].
+ * With a = max |x| over a group of H2O_CKPT_GROUP channels, a code is
+ * 127 x / a rounded to the nearest whole number (ties to even) and the scale
+ * a / 127; the value they stand for is code * scale rounded to the element
+ * type, off by at most a / 254 and that rounding. A group of zeros has scale 0;
+ * a group with a NaN or an infinity stands for NaNs. H2O_ERR_UNSUPPORTED under
+ * H2O_POLICY_INSERT_ALWAYS, whose steps do not attend to the cache they start
+ * from. Asynchronous on `stream`; no allocation. */
+int h2o_checkpoint_save(h2o_ctx *ctx, const void *q, const void *k, const void *v, int T,
+                        void *ckpt, size_t bytes, void *stream);
+
+/* The values a record stands for, in the element type (device; any pointer may
+ * be NULL): q [B,Hq,T,d], k, v [B,Hkv,T,d], K, V [B,Hkv,C,d] with zeros in the
+ * slots n..C-1. T and n are those of the record. The context's cache is neither
+ * read nor changed. Asynchronous on `stream`; no allocation. */
+int h2o_checkpoint_restore(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, int n, void *q,
+                           void *k, void *v, void *K, void *V, void *stream);
+
+/* Backward of a step's chunk attention from its record: what h2o_backward
+ * computes, at the values the record stands for and with the softmax
+ * statistics recomputed from them (the forward's LSE belongs to other keys), so
+ * neither the step's cache nor its LSE is an input and the context's cache is
+ * neither read nor changed. dout = dL/dout [B, Hq, T, d]; writes
+ *   dq [B,Hq,T,d], dK, dV [B,Hkv,C,d] (zero in the slots n..C-1),
+ *   dk, dv [B,Hkv,T,d]
+ * in the element type, each an fp32 sum rounded once, summed over the query
+ * heads of a KV head. Rounding the record's values carries no gradient
+ * (straight-through). NaNs and infinities in the record or in dout spoil the
+ * gradients of their KV head. Device pointers, 16-byte aligned. The first call
+ * (and one with a larger T or n) allocates a workspace; a call captured into a
+ * graph needs one of its size before it. The workspace belongs to the context:
+ * its calls and replays must not overlap on the GPU. Asynchronous on `stream`. */
+int h2o_checkpoint_backward(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, int n,
+                            const void *dout, void *dq, void *dK, void *dV, void *dk, void *dv,
+                            void *stream);
+
+/* The gradient of the cache after a step, handed back through the step's
+ * eviction: for training through a run of steps, last chunk first. token_slot
+ * (device int32 [B, Hkv, T], as h2o_token_slots returned after the step: -1 =
+ * dropped; so is any value outside 0..C-1) and the step's n say where each
+ * entry went; dK, dV, dk, dv are the step's own gradients
+ * (h2o_checkpoint_backward, element type) and gK_next, gV_next (float
+ * [B,Hkv,C,d], both NULL after the last step) those of the cache it left.
+ * Writes, for K and likewise for V,
+ *   gK [B,Hkv,C,d] float: dK[s] + gK_next[s] for s < n if no token was written
+ *     to s, dK[s] if one was, 0 from n on: the gradient of the cache the step
+ *     started from, the next call's gK_next;
+ *   gk [B,Hkv,T,d] element type: dk[t] + gK_next[token_slot[t]], or dk[t] for a
+ *     dropped token: the chunk's whole gradient.
+ * The sums over chunks stay in fp32. gK, gV must not overlap gK_next, gV_next.
+ * Device pointers, 16-byte aligned (token_slot 4). Asynchronous on `stream`; no
+ * allocation. The records of H2O_POLICY_SUM and H2O_POLICY_NORMALIZED steps are
+ * of this form. */
+int h2o_carry_grad(h2o_ctx *ctx, const int32_t *token_slot, int T, int n, const void *dK,
+                   const void *dV, const void *dk, const void *dv, const float *gK_next,
+                   const float *gV_next, float *gK, float *gV, void *gk, void *gv, void *stream);
+
 /* ---- inspection, checkpoint and test hooks ---------------------------- */
 
 /* Candidates of the last step, for each (sequence, KV head): index c < n_prev

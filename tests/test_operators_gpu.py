@@ -1,0 +1,480 @@
+"""The operators next to the step against their definitions in 64 bits
+(operators_ref holds the formulas and derives the tolerances), their edge cases,
+streams, graphs and refusals, and a training run through all of them."""
+import math
+
+import pytest
+import torch
+
+import operators_ref as ref
+from h2o_kv_cache_step_b200 import H2OCache, H2OCheckpoint, H2OError, _lib
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def heads(dtype, B, Hkv, G, d, C, n, T, seed=0):
+    """q, k, v of a chunk and K, V of a cache of C slots, n of them valid; a
+    common part in the keys of a head, as trained models have."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*s):
+        return torch.randn(s, generator=gen, device="cuda")
+
+    lean = normal(B, Hkv, 1, d)
+    q = normal(B, Hkv, G, T, d) + 0.5 * lean[:, :, None]
+    K, V = normal(B, Hkv, C, d) + lean, normal(B, Hkv, C, d)
+    K[:, :, n:] = 0
+    V[:, :, n:] = 0
+    return [x.to(dtype) for x in (q.reshape(B, Hkv * G, T, d), normal(B, Hkv, T, d) + lean, normal(B, Hkv, T, d), K, V)]
+
+
+def cache_of(K, V, Hq, n, max_T=None):
+    B, Hkv, C, d = K.shape
+    c = H2OCache(B, Hq, Hkv, d, C, K.dtype, max_T=max_T)
+    pos = torch.full((B, Hkv, C), -1, dtype=torch.int32, device="cuda")
+    pos[:, :, :n] = torch.arange(n, dtype=torch.int32, device="cuda")
+    c.set_state(K, V, torch.ones((B, Hkv, C), device="cuda"), pos, P=n, n=n)
+    return c
+
+
+def trees(B, T, seed=0, absent=True):
+    gen = torch.Generator().manual_seed(seed)
+    parent = torch.tensor([[int(torch.randint(-1, i, (1,), generator=gen)) if i else -1 for i in range(T)] for _ in range(B)],
+                          dtype=torch.int32)
+    if absent:
+        parent[-1, T - T // 4:] = -2     # fewer nodes in the last sequence
+        if T > 8:
+            parent[0, 3], parent[0, 5] = 3, T  # a node above itself, one out of range: absent
+    return parent.cuda()
+
+
+TREES = [
+    # dtype, B, Hkv, G, d, C, n, T
+    (FP32, 1, 2, 2, 64, 256, 201, 24),
+    (FP32, 2, 1, 3, 128, 50, 0, 9),       # an empty cache
+    (FP32, 1, 1, 1, 64, 1, 1, 1),         # one slot, one node
+    (BF16, 1, 8, 4, 128, 2048, 2048, 1),  # one token
+    (BF16, 3, 2, 4, 128, 700, 643, 1),
+    (BF16, 2, 2, 1, 64, 64, 64, 1),       # one row to a KV head
+    (BF16, 2, 3, 2, 64, 300, 257, 5),     # a few nodes, a page of one slot at the end
+    (BF16, 4, 2, 4, 128, 1000, 901, 61),
+    (BF16, 1, 2, 3, 64, 129, 128, 43),    # rows 128 and 129 of a group
+    (BF16, 1, 1, 8, 128, 128, 127, 16),
+    (BF16, 2, 2, 3, 128, 300, 0, 77),     # an empty cache: the tree alone
+    (BF16, 1, 2, 4, 64, 4000, 3999, 255),
+    (BF16, 1, 2, 8, 128, 5000, 4097, 256),
+    (BF16, 2, 1, 1, 128, 40, 33, 256),    # a tree longer than the cache
+]
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,C,n,T", TREES)
+def test_tree_attention(dtype, B, Hkv, G, d, C, n, T):
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=T)
+    parent = trees(B, T, seed=n)
+    c = cache_of(K, V, Hkv * G, n)
+    before = c.get_state()
+    out, lse = c.tree_attend(q, k, v, parent)
+    c.sync_check()
+    want, wlse, bound, lbound = ref.tree(q, k, v, parent, K, V, n, dtype)
+    ref.within("out", out, want, bound)
+    there = wlse > -math.inf
+    assert torch.equal(there, lse > -math.inf)
+    assert not out[~there].any()
+    ref.within("lse", lse[there], wlse[there], lbound[there])
+    again = c.tree_attend(q, k, v, parent)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    for a, b in zip(before, c.get_state()):
+        assert torch.equal(a, b) if torch.is_tensor(a) else a == b
+
+
+@pytest.mark.parametrize("dtype,G,d,n,T", [(FP32, 2, 64, 70, 12), (BF16, 4, 128, 700, 3), (BF16, 4, 128, 700, 40), (BF16, 2, 64, 130, 200)])
+def test_tree_keys_that_a_row_does_not_see_leave_it_alone(dtype, G, d, n, T):
+    B, Hkv, C = 2, 2, 800
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=5)
+    parent = trees(B, T, seed=6)
+    clean = cache_of(K, V, Hkv * G, n).tree_attend(q, k, v, parent)
+    see = ref.ancestors(parent).cuda()
+    K[:, :, n:], V[:, :, n:] = math.nan, math.inf
+    for b, node, kv, ww in ((0, T // 2, math.nan, 1.0), (1, T - 1, math.inf, math.nan), (0, T - 1, 0.0, -math.inf),
+                          (0, 1, math.nan, 1.0), (1, 2, 0.0, math.nan)):
+        k[b, :, node] += kv
+        v[b, :, node] *= ww
+    hit = torch.zeros((B, T), dtype=torch.bool, device="cuda")
+    for b, node in ((0, T // 2), (1, T - 1), (0, T - 1), (0, 1), (1, 2)):
+        hit[b] |= see[b, :, node]
+    out, lse = cache_of(K, V, Hkv * G, n).tree_attend(q, k, v, parent)
+    ok = ~hit[:, None].expand(B, Hkv * G, T)
+    assert 0 < int(ok.sum()) < ok.numel()
+    assert torch.equal(out[ok], clean[0][ok]) and torch.equal(lse[ok], clean[1][ok])
+    assert not out[~ok].isfinite().all(-1).any()
+
+
+def test_tree_bad_slots_and_queries_are_not_hidden():
+    """A NaN in a valid slot reaches every row of its KV head, one in a query its
+    own row; an infinite logit is NaN as in the definition."""
+    for T in (1, 40):
+        q, k, v, K, V = heads(BF16, 1, 2, 4, 128, 512, 512, T, seed=2)
+        parent = trees(1, T, absent=False)
+        clean = cache_of(K, V, 8, 512).tree_attend(q, k, v, parent)[0]
+        for value in (math.nan, math.inf):
+            bad = K.clone()
+            bad[0, 1, 300, 7] = value
+            out, lse = cache_of(bad, V, 8, 512).tree_attend(q, k, v, parent)
+            assert torch.equal(out[:, :4], clean[:, :4])
+            # an infinite key gives a row +inf or -inf by its query's sign; -inf drops the key
+            seen = torch.ones((4, T), dtype=torch.bool, device="cuda") if value != value else q[0, 4:, :, 7] > 0
+            assert out[0, 4:][seen].isnan().all() and lse[0, 4:][seen].isnan().all()
+            assert out[0, 4:][~seen].isfinite().all()
+        qb = q.clone()
+        qb[0, 5, T - 1, 3] = math.nan
+        out = cache_of(K, V, 8, 512).tree_attend(qb, k, v, parent)[0]
+        assert out[0, 5, T - 1].isnan().all()
+        out[0, 5, T - 1] = clean[0, 5, T - 1]
+        assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_tree_with_no_node_in_it(T):
+    q, k, v, K, V = heads(BF16, 2, 2, 2, 64, 256, 200, T)
+    parent = torch.full((2, T), -2, dtype=torch.int32, device="cuda")
+    parent[0, 1:] = 0                      # under an absent node: absent too
+    out, lse = cache_of(K, V, 4, 200).tree_attend(q, k, v, parent)
+    assert not out.any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype,T", [(FP32, 20), (BF16, 4), (BF16, 130)])
+def test_a_chain_is_what_the_step_computes(dtype, T):
+    """One path of T nodes: rows as of the step that commits it."""
+    q, k, v, K, V = heads(dtype, 2, 2, 4, 128, 384, 380, T, seed=9)
+    c = cache_of(K, V, 8, 380)
+    parent = (torch.arange(T, dtype=torch.int32, device="cuda") - 1).expand(2, T).contiguous()
+    out, lse = c.tree_attend(q, k, v, parent)
+    step = c.step(q, k, v)
+    _, _, bound, lbound = ref.tree(q, k, v, parent, K, V, 380, dtype)
+    extra = 1e-4 if dtype == BF16 else 0.0  # the step's polynomial exponentials: 7.7e-5 each
+    ref.within("out", out, step.double(), 2 * bound + 2 * extra * V.abs().max())
+    ref.within("lse", lse, c.lse().double(), 2 * lbound + extra)
+
+
+# ---- checkpoints ------------------------------------------------------------------
+RECORDS = [
+    # dtype, B, Hkv, G, d, C, n, T
+    (FP32, 1, 2, 2, 64, 256, 256, 64),
+    (FP32, 2, 1, 1, 128, 9, 0, 1),
+    (BF16, 1, 8, 4, 128, 300, 300, 129),
+    (BF16, 3, 2, 3, 64, 100, 77, 31),
+    (BF16, 1, 1, 1, 64, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,C,n,T", RECORDS)
+def test_checkpoint_codes_scales_and_values(dtype, B, Hkv, G, d, C, n, T):
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=n + T)
+    q[0, 0, 0, :32] = 0                                       # a group of zeros
+    k[0, 0, 0, :32] = torch.arange(32, device="cuda") * 0.5   # codes next to and on borders
+    k[0, 0, 0, 31] = 127.0
+    v[0, 0, 0, 32:64] = 2e-41 * torch.arange(32, device="cuda")  # subnormal
+    v[0, 0, 0, :32] = 3e38
+    v[0, 0, 0, 1:32:2] = -1.5e38
+    q[-1, -1, -1, 40] = math.nan
+    q[-1, -1, -1, 1] = math.inf
+    c = cache_of(K, V, Hkv * G, n)
+    ck = c.checkpoint(q, k, v)
+    assert ck.n == n and ck.T == T and ck.nbytes == sum(x.numel() for x in (q, k, v)) * 9 // 8 + 2 * B * Hkv * n * d * 9 // 8
+    xs = [q, k, v, K[:, :, :n], V[:, :, :n]]
+    want = [ref.quantise(x) for x in xs]
+    for name, got, w in zip("qkvKV", ck.codes(), want):
+        assert torch.equal(got, w[0]), name
+    for name, got, w in zip("qkvKV", ck.scales(), want):
+        assert torch.equal(got.nan_to_num(nan=-1), w[1].nan_to_num(nan=-1)), name
+    back = c.checkpoint_restore(ck)
+    c.sync_check()
+    for name, got, w, x in zip("qkvKV", back, want, xs):
+        w = w[2]
+        if name in "KV":
+            assert got.shape[2] == C and not got[:, :, n:].any()
+            got = got[:, :, :n]
+        assert torch.equal(got.nan_to_num(nan=-1), w.nan_to_num(nan=-1)), name
+        assert torch.equal(got.isnan(), w.isnan())
+
+
+def test_checkpoint_outlives_the_cache_it_was_taken_from():
+    q, k, v, K, V = heads(BF16, 1, 2, 2, 64, 64, 64, 16)
+    c = cache_of(K, V, 4, 64)
+    ck = c.checkpoint(q, k, v)
+    first = c.checkpoint_restore(ck)
+    c.step(q, k, v)
+    c.reset()
+    for a, b in zip(first, c.checkpoint_restore(ck)):
+        assert torch.equal(a, b)
+    other = H2OCache(1, 4, 2, 64, 80, BF16)   # more slots: the record's, then zeros
+    K2 = other.checkpoint_restore(ck)[3]
+    assert torch.equal(K2[:, :, :64], first[3]) and not K2[:, :, 64:].any()
+
+
+BACKWARDS = [
+    # dtype, B, Hkv, G, d, C, n, T
+    (FP32, 1, 2, 2, 64, 256, 256, 64),
+    (FP32, 2, 1, 3, 128, 40, 33, 17),
+    (FP32, 1, 1, 1, 64, 5, 0, 1),         # a row that sees itself alone: dq and dk are zero
+    (BF16, 1, 1, 1, 64, 5, 0, 1),
+    (BF16, 1, 2, 2, 128, 40, 0, 130),     # an empty cache
+    (BF16, 2, 2, 8, 64, 300, 257, 77),
+    (BF16, 2, 3, 3, 128, 200, 127, 129),
+    (BF16, 1, 2, 4, 128, 512, 512, 256),
+    (BF16, 1, 2, 1, 64, 1000, 999, 1),
+    (BF16, 1, 1, 4, 128, 2000, 1921, 300),
+    (BF16, 3, 1, 5, 64, 128, 128, 383),
+]
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,C,n,T", BACKWARDS)
+def test_backward_from_a_checkpoint(dtype, B, Hkv, G, d, C, n, T):
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=n + T)
+    c = cache_of(K, V, Hkv * G, n)
+    ck = c.checkpoint(q, k, v)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(dtype)
+    rest = c.checkpoint_restore(ck)
+    c.reset()                              # the cache plays no part
+    got = c.checkpoint_backward(ck, dout)
+    c.sync_check()
+    want, bound = ref.backward(*rest, dout, n, dtype)
+    for name, g, w, b in zip(("dq", "dK", "dV", "dk", "dv"), got, want, bound):
+        assert g.dtype == dtype
+        if name in ("dK", "dV"):
+            assert g.shape[2] == C and not g[:, :, n:].any()
+            g = g[:, :, :n]
+        ref.within(name, g, w, b)
+    for a, b in zip(got, c.checkpoint_backward(ck, dout)):
+        assert torch.equal(a, b)
+
+
+def test_backward_of_equal_keys():
+    """Every key the same: dq is zero up to the roundings of its operands."""
+    q, k, v, K, V = heads(BF16, 1, 1, 2, 64, 256, 256, 128)
+    k[:], K[:] = k[:, :, :1], k[:, :, :1]
+    c = cache_of(K, V, 2, 256)
+    ck = c.checkpoint(q, k, v)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(BF16)
+    want, bound = ref.backward(*c.checkpoint_restore(ck), dout, 256, BF16)
+    for name, g, w, b in zip(("dq", "dK", "dV", "dk", "dv"), c.checkpoint_backward(ck, dout), want, bound):
+        ref.within(name, g, w, b)
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,d,C,n,T", [(FP32, 2, 3, 64, 300, 251, 77), (BF16, 1, 2, 128, 33, 33, 100),
+                                                  (BF16, 2, 1, 64, 1, 0, 1), (BF16, 1, 2, 128, 500, 499, 1)])
+@pytest.mark.parametrize("last", [False, True])
+def test_carry(dtype, B, Hkv, d, C, n, T, last):
+    gen = torch.Generator(device="cuda").manual_seed(C + T)
+
+    def normal(t, *s):
+        return torch.randn(s, generator=gen, device="cuda").to(t)
+
+    dK, dV, dk, dv = [normal(dtype, B, Hkv, x, d) for x in (C, C, T, T)]
+    g = [None, None] if last else [normal(FP32, B, Hkv, C, d) for _ in range(2)]
+    slots = torch.full((B, Hkv, T), -1, dtype=torch.int32)
+    for b in range(B):
+        for h in range(Hkv):
+            k = min(T, C) // 2 + 1
+            at = torch.randperm(T, generator=torch.Generator().manual_seed(b + 7 * h))[:min(k, T)]
+            slots[b, h, at] = torch.randperm(C, generator=torch.Generator().manual_seed(b + 9 * h))[:len(at)].int()
+            slots[b, h, T // 3] = -5 if h else C + 3  # outside the cache: dropped
+    c = H2OCache(B, Hkv, Hkv, d, C, dtype)
+    gK, gV, gk, gv = c.carry_grad(slots.cuda(), n, dK, dV, dk, dv, *g)
+    c.sync_check()
+    # one addition in fp32 and one rounding to the element type: exact ties aside, equal
+    for got, tok, own, ch, nxt in ((gK, gk, dK, dk, g[0]), (gV, gv, dV, dv, g[1])):
+        before, chunk = ref.carry(slots, n, own, ch, nxt)
+        ref.within("cache", got, before, ref.U32 * before.abs())
+        ref.within("chunk", tok, chunk, (ref.U[dtype] + 2 * ref.U32) * chunk.abs())
+
+
+# ---- together -----------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_training_run(dtype):
+    """Five chunks through checkpoint and step, then backward and carry, last
+    chunk first, against autograd in 64 bits through the whole run: the cache's
+    contents are replayed with the recorded slots, and every chunk attends to
+    the values its record stands for (straight through)."""
+    B, Hkv, G, d, C, T, steps = 2, 2, 2, 64, 96, 40, 5
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    c = H2OCache(B, Hkv * G, Hkv, d, C, dtype)
+    chunks, records, slots, ns, douts = [], [], [], [], []
+    for _ in range(steps):
+        q, k, v = (torch.randn((B, h, T, d), generator=gen, device="cuda").to(dtype) for h in (Hkv * G, Hkv, Hkv))
+        records.append(c.checkpoint(q, k, v))
+        ns.append(c.counters()[1])
+        out = c.step(q, k, v)
+        slots.append(c.token_slots())
+        douts.append(torch.randn(out.shape, generator=gen, device="cuda").to(dtype))
+        chunks.append((q, k, v))
+    got, gK, gV = [None] * steps, None, None
+    for i in reversed(range(steps)):
+        dq, dK, dV, dk, dv = c.checkpoint_backward(records[i], douts[i])
+        gK, gV, gk, gv = c.carry_grad(slots[i], ns[i], dK, dV, dk, dv, gK, gV)
+        got[i] = (dq, gk, gv)
+    c.sync_check()
+    assert ns == [0, 40, 80, 96, 96]
+
+    leaves = [[x.double().requires_grad_() for x in ch] for ch in chunks]
+    K = torch.zeros((B, Hkv, C, d), dtype=torch.float64, device="cuda")
+    V = torch.zeros_like(K)
+    total = 0.0
+    for i in range(steps):
+        n, rest = ns[i], [x.double() for x in c.checkpoint_restore(records[i])]
+        q, k, v = leaves[i]
+        use = [a + (b - a).detach() for a, b in zip((q, k, v, K, V), rest)]
+        s = torch.einsum("bghtd,bgjd->bghtj", use[0].view(B, Hkv, G, T, d), torch.cat([use[3][:, :, :n], use[1]], 2)) / math.sqrt(d)
+        s = s.masked_fill(torch.arange(n + T, device="cuda") - n > torch.arange(T, device="cuda")[:, None], -math.inf)
+        o = torch.einsum("bghtj,bgjd->bghtd", torch.softmax(s, -1), torch.cat([use[4][:, :, :n], use[2]], 2))
+        total = total + (o.reshape(B, Hkv * G, T, d) * douts[i].double()).sum()
+        at = slots[i].long()
+        put = (at[..., None] == torch.arange(C, device="cuda")).double()       # [B,Hkv,T,C]
+        keep = (1 - put.sum(2))[..., None]
+        K = K * keep + torch.einsum("bgtc,bgtd->bgcd", put, k)
+        V = V * keep + torch.einsum("bgtc,bgtd->bgcd", put, v)
+    total.backward()
+    # each of the up to 5 terms of a gradient carries the relative roundings of a
+    # backward: fp32 sums of a few hundred products (1e-4 of the largest value is
+    # far above their worst), bf16 operands and results (3 half steps of the term)
+    tol = {FP32: 1e-4, BF16: 3 * 5 * 2.0**-8}[dtype]
+    for i in range(steps):
+        for name, g, leaf in zip("qkv", got[i], leaves[i]):
+            w = leaf.grad
+            assert float((g.double() - w).abs().max()) <= tol * float(w.abs().max()), (i, name)
+
+
+def test_draft_verify_commit():
+    """A serving loop: draft a tree, verify it, commit one path with the step;
+    the committed rows agree with the tree's."""
+    B, Hkv, G, d, C, T = 2, 2, 4, 128, 256, 12
+    q, k, v, K, V = heads(BF16, B, Hkv, G, d, C, 256, T, seed=3)
+    c = cache_of(K, V, Hkv * G, 256)
+    path = [0, 2, 5, 9]
+    parent = torch.full((B, T), -1, dtype=torch.int32)
+    for a, b in zip(path, path[1:]):
+        parent[:, b] = a
+    parent[:, 11], parent[:, 7] = 2, 0
+    out, _ = c.tree_attend(q, k, v, parent.cuda())
+    qc, kc, vc = (x[:, :, path].contiguous() for x in (q, k, v))
+    step = c.step(qc, kc, vc)
+    chain = (torch.arange(4, dtype=torch.int32, device="cuda") - 1).expand(B, 4).contiguous()
+    _, _, bound, _ = ref.tree(qc, kc, vc, chain, K, V, 256, BF16)
+    ref.within("committed rows", out[:, :, path], step.double(), 2 * bound + 1e-4 * V.abs().max())
+    assert c.counters()[0] == 260
+
+
+# ---- streams, graphs, refusals --------------------------------------------------------
+def calls(dtype=BF16, T=40):
+    q, k, v, K, V = heads(dtype, 2, 2, 4, 128, 300, 290, T, seed=1)
+    c = cache_of(K, V, 8, 290)
+    parent = trees(2, T)
+    ck = c.checkpoint(q, k, v)
+    dout = torch.randn_like(q)
+    dK, dV, dk, dv = [torch.randn_like(x) for x in (K, V, k, v)]
+    g = [torch.randn(K.shape, device="cuda") for _ in range(2)]
+    slots = torch.full((2, 2, T), -1, dtype=torch.int32, device="cuda")
+    slots[:, :, 1] = 7
+    return c, {
+        "tree": lambda **kw: c.tree_attend(q, k, v, parent, **kw),
+        "checkpoint": lambda **kw: (c.checkpoint(q, k, v, **kw).buffer,),
+        "restore": lambda **kw: c.checkpoint_restore(ck, **kw),
+        "backward": lambda **kw: c.checkpoint_backward(ck, dout, **kw),
+        "carry": lambda **kw: c.carry_grad(slots, 290, dK, dV, dk, dv, *g, **kw),
+    }
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("T", [2, 40])
+def test_on_another_stream_and_replayed_from_a_graph(dtype, T):
+    c, ops = calls(dtype, T)
+    want = {name: op() for name, op in ops.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for name, op in ops.items():
+        got = op(stream=side)
+        side.synchronize()
+        for a, b in zip(want[name], got):
+            assert torch.equal(a, b), name
+    for name, op in ops.items():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = op()
+        for _ in range(2):
+            for x in got:
+                x.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(want[name], got):
+                assert torch.equal(a, b), name
+        del graph
+
+
+def test_a_captured_backward_needs_its_workspace_first():
+    q, k, v, K, V = heads(BF16, 1, 2, 2, 64, 64, 64, 32)
+    c = cache_of(K, V, 4, 64)
+    ck, dout = c.checkpoint(q, k, v), torch.randn_like(q)
+    with pytest.raises(H2OError, match="outside a capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            q.add_(0)  # the graph is not empty
+            c.checkpoint_backward(ck, dout)
+    graph = torch.cuda.CUDAGraph()
+    want = c.checkpoint_backward(ck, dout)
+    with torch.cuda.graph(graph):
+        got = c.checkpoint_backward(ck, dout)
+    # a larger call takes a new workspace; the graph keeps the old one
+    big = heads(BF16, 1, 2, 2, 64, 64, 64, 200)
+    c.checkpoint_backward(c.checkpoint(*big[:3]), torch.randn_like(big[0]))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_refusals():
+    q, k, v, K, V = heads(BF16, 1, 2, 2, 64, 64, 50, 8)
+    c = cache_of(K, V, 4, 50)
+    parent = trees(1, 8)
+    L, P = _lib.lib(), lambda t: t.data_ptr()
+    out, lse = torch.empty_like(q), torch.empty((1, 4, 8), device="cuda")
+    assert L.h2o_tree_attend(c.handle, P(q), P(k), P(v), P(parent), P(out), P(lse), 0, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_tree_attend(c.handle, P(q), P(k), P(v), P(parent), P(out), P(lse), 257, None) == _lib.H2O_ERR_UNSUPPORTED
+    assert L.h2o_tree_attend(c.handle, P(q), P(k), P(v), None, P(out), P(lse), 8, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_tree_attend(c.handle, P(q) + 2, P(k), P(v), P(parent), P(out), P(lse), 7, None) == _lib.H2O_ERR_ALIGN
+    assert L.h2o_tree_attend(c.handle, P(q), P(k), P(v), P(parent), P(out), P(lse) + 2, 7, None) == _lib.H2O_ERR_ALIGN
+    ck = c.checkpoint(q, k, v)
+    args = (P(q), P(k), P(v), P(K), P(V), None)
+    assert L.h2o_checkpoint_save(c.handle, P(q), P(k), P(v), 8, P(ck.buffer), ck.nbytes - 1, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(c.handle, P(ck.buffer), ck.nbytes, 8, 65, *args) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(c.handle, P(ck.buffer), ck.nbytes, 8, -1, *args) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(c.handle, P(ck.buffer), ck.nbytes, 9, 50, *args) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(c.handle, P(ck.buffer), ck.nbytes, 8, 50, *[None] * 6) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(c.handle, P(ck.buffer) + 4, ck.nbytes, 8, 50, *args) == _lib.H2O_ERR_ALIGN
+    g = [torch.zeros(K.shape, device="cuda") for _ in range(3)]
+    slots = torch.full((1, 2, 8), -1, dtype=torch.int32, device="cuda")
+    rest = (P(K), P(V), P(k), P(v))
+    assert L.h2o_carry_grad(c.handle, P(slots), 8, 50, *rest, P(g[0]), None, P(g[1]), P(g[2]), P(k), P(v), None) == _lib.H2O_ERR_ARG
+    assert L.h2o_carry_grad(c.handle, P(slots), 8, 50, *rest, P(g[0]), P(g[0]), P(g[0]), P(g[2]), P(k), P(v), None) == _lib.H2O_ERR_ARG
+    with pytest.raises(ValueError):
+        c.tree_attend(q.transpose(2, 3).contiguous().transpose(2, 3), k, v, parent)
+    with pytest.raises(ValueError):
+        c.tree_attend(q, k, v, parent.long())
+    with pytest.raises(ValueError):
+        c.checkpoint_backward(ck, torch.zeros((1, 4, 9, 64), dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError):
+        H2OCheckpoint(ck.buffer[:-1], 1, 4, 2, 64, 8, 50)
+    c.set_policy(_lib.H2O_POLICY_INSERT_ALWAYS)
+    with pytest.raises(H2OError, match="insert-always"):
+        c.tree_attend(q, k, v, parent)
+    with pytest.raises(H2OError, match="insert-always"):
+        c.checkpoint(q, k, v)
+    c.sync_check()

@@ -1,0 +1,115 @@
+"""Refusals of the operators next to the step, and the 64-bit backward the GPU
+tests compare with against differences (no GPU needed)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import operators_ref as ref
+from h2o_kv_cache_step_b200 import H2OCache, H2OCheckpoint, _lib
+
+
+@pytest.fixture(scope="module")
+def L():
+    from h2o_kv_cache_step_b200 import build
+    build.build()
+    return _lib.lib()
+
+
+def test_null_context_is_an_argument_error(L):
+    assert L.h2o_tree_attend(None, None, None, None, None, None, None, 4, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_bytes(None, 4, 4, ctypes.byref(ctypes.c_size_t())) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_save(None, None, None, None, 4, None, 0, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_restore(None, None, 0, 4, 4, None, None, None, None, None, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_checkpoint_backward(None, None, 0, 4, 4, None, None, None, None, None, None, None) == _lib.H2O_ERR_ARG
+    assert L.h2o_carry_grad(None, None, 4, 4, *[None] * 11) == _lib.H2O_ERR_ARG
+
+
+def test_constants_match_the_header():
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(_lib.PKG), "include", "h2o.h")).read()
+    assert int(re.search(r"#define H2O_TREE_MAX_T (\d+)", src).group(1)) == _lib.H2O_TREE_MAX_T
+    assert int(re.search(r"#define H2O_CKPT_GROUP (\d+)", src).group(1)) == _lib.H2O_CKPT_GROUP
+
+
+class _Never:
+    """Stands in for a context that no refused call may reach."""
+    B, Hq, Hkv, d, C, dtype = 2, 4, 2, 64, 32, torch.bfloat16
+    device = torch.device("cuda", 0)
+    _need = H2OCache._need
+    _record = H2OCache._record
+
+    def __getattr__(self, name):
+        raise AssertionError(f"the call went on to {name}")
+
+
+def _t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_host_tensors_and_wrong_shapes_are_refused():
+    c = _Never()
+    with pytest.raises(ValueError, match="q: need"):
+        H2OCache.tree_attend(c, _t(2, 4, 5), _t(2, 2, 5, 64), _t(2, 2, 5, 64), _t(2, 5, dtype=torch.int32))
+    with pytest.raises(ValueError, match="q: need a contiguous"):
+        H2OCache.tree_attend(c, _t(2, 4, 5, 64), _t(2, 2, 5, 64), _t(2, 2, 5, 64), _t(2, 5, dtype=torch.int32))
+    with pytest.raises(ValueError, match="token_slots: need"):
+        H2OCache.carry_grad(c, _t(2, 5, dtype=torch.int32), 3, *[_t(2, 2, 5, 64)] * 4)
+    with pytest.raises(ValueError, match="token_slots: need a contiguous"):
+        H2OCache.carry_grad(c, _t(2, 2, 5, dtype=torch.int32), 3, *[_t(2, 2, 5, 64)] * 4)
+
+
+def test_a_record_of_another_size_or_place_is_refused():
+    rows = 2 * (4 * 5 + 2 * 2 * 5 + 2 * 2 * 3)
+    with pytest.raises(ValueError, match="buffer: need"):
+        H2OCheckpoint(torch.zeros(rows * (64 + 8), dtype=torch.uint8), 2, 4, 2, 64, 5, 3)
+    ck = H2OCheckpoint.__new__(H2OCheckpoint)
+    ck.buffer, ck.shape, ck.T, ck.n = torch.zeros(rows * 72, dtype=torch.uint8), (2, 4, 2, 64), 5, 3
+    with pytest.raises(ValueError, match="checkpoint: of"):
+        H2OCache._record(_Never(), ck)
+    ck.shape = (2, 4, 4, 64)
+    with pytest.raises(ValueError, match="checkpoint: of"):
+        H2OCache._record(_Never(), ck)
+
+
+def test_a_record_splits_into_its_sections():
+    """codes() and scales() find the five sections where the layout puts them."""
+    B, Hq, Hkv, d, T, n = 2, 4, 2, 64, 5, 3
+    gen = torch.Generator().manual_seed(1)
+    xs = [torch.randn(s, generator=gen) for s in ((B, Hq, T, d), (B, Hkv, T, d), (B, Hkv, T, d), (B, Hkv, n, d), (B, Hkv, n, d))]
+    codes, scales, _ = zip(*[ref.quantise(x) for x in xs])
+    ck = H2OCheckpoint.__new__(H2OCheckpoint)
+    ck.buffer = torch.cat([c.reshape(-1).view(torch.uint8) for c in codes] + [s.reshape(-1).view(torch.uint8) for s in scales])
+    ck.shape, ck.T, ck.n = (B, Hq, Hkv, d), T, n
+    for a, b in zip(ck.codes(), codes):
+        assert torch.equal(a, b)
+    for a, b in zip(ck.scales(), scales):
+        assert torch.equal(a, b)
+
+
+def test_reference_backward_against_differences():
+    """d/dx of sum(out * dout) by central differences, step 1e-5: off by about
+    1e-10 (the third derivative times the step squared) and 1e-16 / 1e-5 of the
+    sum's size, far below 1e-6."""
+    B, Hkv, G, T, n, d = 1, 2, 2, 5, 4, 32
+    gen = torch.Generator().manual_seed(3)
+    xs = [torch.randn(s, generator=gen, dtype=torch.float64)
+          for s in ((B, Hkv * G, T, d), (B, Hkv, T, d), (B, Hkv, T, d), (B, Hkv, n, d), (B, Hkv, n, d))]
+    do = torch.randn((B, Hkv * G, T, d), generator=gen, dtype=torch.float64)
+
+    def loss(q, k, v, K, V):
+        s = torch.einsum("bghtd,bgjd->bghtj", q.view(B, Hkv, G, T, d), torch.cat([K, k], 2)) / math.sqrt(d)
+        s = s.masked_fill(torch.arange(n + T) - n > torch.arange(T)[:, None], -math.inf)
+        o = torch.einsum("bghtj,bgjd->bghtd", torch.softmax(s, -1), torch.cat([V, v], 2))
+        return float((o.reshape(B, Hkv * G, T, d) * do).sum())
+
+    dq, dK, dV, dk, dv = ref.backward(*xs, do, n, torch.float32)[0]
+    for i, g in enumerate((dq, dk, dv, dK, dV)):
+        for _ in range(12):
+            at = tuple(int(torch.randint(x, (1,), generator=gen)) for x in g.shape)
+            lo, hi = [x.clone() for x in xs], [x.clone() for x in xs]
+            lo[i][at] -= 1e-5
+            hi[i][at] += 1e-5
+            assert abs((loss(*hi) - loss(*lo)) / 2e-5 - float(g[at])) < 1e-6
