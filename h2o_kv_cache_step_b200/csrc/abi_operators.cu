@@ -202,7 +202,7 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
         return at;
     };
     const size_t oq = take(nq * c->elem), ok = take(nk * c->elem), ov = take(nk * c->elem);
-    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float4) * (nq / c->d));
+    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(c->B, c->Hq, T));
     rc = checkpoint_workspace(c, end, s);
     if (rc != H2O_OK) return rc;
     char* w = static_cast<char*>(c->ckpt_ws);
@@ -237,12 +237,12 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     a.dV = dV;
     a.dk = dk;
     a.dv = dv;
-    a.stats = reinterpret_cast<float4*>(w + os);
+    a.stats = reinterpret_cast<float*>(w + os);
     a.wb.err_word = c->err_dev;
     a.wb.ns = c->wait_ns;
     a.stream = s;
     a.num_sms = c->num_sms;
-    H2O_TRY(c, launch_ckpt_backward_simt(a), "launch checkpoint backward");
+    H2O_TRY(c, c->use_tc ? launch_ckpt_backward_tc(a) : launch_ckpt_backward_simt(a), "launch checkpoint backward");
     return H2O_OK;
 }
 

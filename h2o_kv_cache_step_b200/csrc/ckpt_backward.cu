@@ -245,12 +245,14 @@ cudaError_t backward_typed(const CkptBwdArgs& a) {
     const int G = a.Hq / a.Hkv, groups = a.B * a.Hkv;
     const int rows = (G * a.T + kRows - 1) / kRows, keys = (a.C + a.T + kKeys - 1) / kKeys;
     ckpt_dq_simt_kernel<E, D><<<groups * rows, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq, a.stats, G,
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq,
+        reinterpret_cast<float4*>(a.stats), G,
         a.T, a.n, a.pitch, rows, scale_log2, scale);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ckpt_dkdv_simt_kernel<E, D><<<groups * keys, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, a.stats, (E*)a.dK,
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
+        reinterpret_cast<const float4*>(a.stats), (E*)a.dK,
         (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n, a.pitch, keys, scale_log2, scale);
     return cudaGetLastError();
 }

@@ -78,12 +78,16 @@ struct CkptBwdArgs {
     void* dV;
     void* dk;           // [B,Hkv,T,d]
     void* dv;
-    float4* stats;      // [B,Hq,T]: log2-domain maximum, 1 / sum, D, unused
+    float* stats;       // workspace of ckpt_stats_floats() floats
     WaitBound wb;
     cudaStream_t stream;
     int num_sms;
 };
+// Statistics of every query row: rows padded to whole 128-row tiles (tensor
+// cores: -log2 of the sum of exponentials, then D), or four floats a row.
+inline size_t ckpt_stats_floats(int B, int Hq, int T) { return (size_t)B * Hq * ((T + 127) / 128 * 128) * 4; }
 cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a);
+cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a);  // bf16
 
 // Gradient of the cache after a step handed back through the eviction.
 struct CarryArgs {
