@@ -103,6 +103,11 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     if ((reinterpret_cast<uintptr_t>(parent) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3))
         return fail(c, H2O_ERR_ALIGN, "parent and lse must be 4-byte aligned");
     DeviceGuard g(c->device);
+    if (c->use_tc && !c->tree_part) {
+        if (capturing((cudaStream_t)stream))
+            return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
+        H2O_TRY(c, cudaMalloc(&c->tree_part, sizeof(float) * tree_part_floats(c->num_sms, c->d)), "cudaMalloc(tree workspace)");
+    }
     TreeArgs a{};
     a.B = c->B;
     a.Hq = c->Hq;
@@ -120,11 +125,12 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     a.Vc = c->Vc;
     a.out = out;
     a.lse = lse;
+    a.part = c->tree_part;
     a.wb.err_word = c->err_dev;
     a.wb.ns = c->wait_ns;
     a.stream = (cudaStream_t)stream;
     a.num_sms = c->num_sms;
-    H2O_TRY(c, launch_tree_simt(a), "launch tree attention");
+    H2O_TRY(c, c->use_tc ? launch_tree_tc(a) : launch_tree_simt(a), "launch tree attention");
     return H2O_OK;
 }
 

@@ -5,13 +5,24 @@
 //   code = rint(127 x / a) (ties to even), scale = a / 127 rounded to fp32,
 // and the value it stands for is code * scale, rounded to the element type. A
 // group of zeros has scale 0; a group with a NaN or an infinity has scale NaN
-// and stands for NaNs. The quotient decides the code, so it is taken where its
-// rounding cannot move it across a border k + 1/2: 127 x is exact in fp32 for a
-// bf16 x, and 254 x - (2k + 1) a is a whole number of units of the last place of
-// two 8-bit significands, so an fp32 quotient (24 bits) falls on the real
-// quotient's side; fp32 inputs take the quotient in 64 bits for the same reason.
+// and stands for NaNs.
 //
-// Both directions are bound by memory: each value is read and written once.
+// The code follows the real quotient without a division per value. With p-bit
+// significands (8 for bf16, 24 for fp32), 254 x - (2k + 1) a is a whole number
+// of units of x's last place, so a quotient that is not on a border k + 1/2
+// keeps a relative distance of 2^-(8 + p) from it; x times the rounded 127 / a
+// is within 2^-23 of it in fp32 and 2^-52 in 64 bits, so its nearest whole number
+// is the code. What is left are the borders, (2k + 1) a = 254 x:
+//   bf16, in fp32: 127 is prime, so it divides 2k + 1 (then k = 63 and x = a / 2)
+//   or a's significand (then that is 127 times a power of two, and 127 / a is
+//   exact). With 127 / a rounded up, the first lands on 63.5 or just above it
+//   and goes to 64, the even one, and the second is exact: one multiply-add and
+//   its rounding give the code.
+//   fp32, in 64 bits: the remainder 127 x - code a is exact, is +-a / 2 on a
+//   border, and an odd code then moves to its even neighbour.
+//
+// Both directions are bound by memory: each value is read and written once, 32
+// or 64 bytes of it per thread.
 #include <math.h>
 
 #include "operators.h"
@@ -21,181 +32,191 @@ namespace h2o {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPer = 16;  // values per thread; two threads share a group of 32
+static_assert(kCkptGroup == 2 * kPer, "a group is a pair of threads");
 
-// The five sections of a record in order, as row counts and first rows.
+// The five sections of a record (q, k, v, K, V): `outer` runs of `rows` rows in
+// the record, and of `pitch` rows in the tensors (rows past `rows` are empty).
+struct Section {
+    void* x;
+    unsigned long long code_row;  // first row in the record
+    unsigned long long rows, pitch;
+    int blocks;      // per run
+    int block_end;   // first block after the section
+};
 struct Sections {
-    unsigned long long end[5];  // first row after the section (record rows)
-    int block_end[5];           // first block after the section
+    Section s[5];
 };
 
-__device__ __forceinline__ int section_of(const Sections& s, int block) {
+// Where a thread works: its section, its rows and its first channel.
+struct Place {
+    void* x;
+    unsigned long long code, row;  // row in the record, row in the tensor
+    int col;
+    bool in, valid;  // a row of the tensor; one that the record holds
+};
+
+template <int D>
+__device__ __forceinline__ Place place(const Sections& sec) {
+    constexpr int kRows = kThreads * kPer / D;  // per block
     int k = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) k += block >= s.block_end[i];
-    return k;
+    for (int i = 0; i < 4; ++i) k += (int)blockIdx.x >= sec.s[i].block_end;
+    const Section& s = sec.s[k];
+    const int blk = blockIdx.x - (k ? sec.s[k - 1].block_end : 0);
+    const unsigned long long run = blk / s.blocks;
+    const unsigned long long r = (unsigned long long)(blk % s.blocks) * kRows + threadIdx.x / (D / kPer);
+    Place p;
+    p.x = s.x;
+    p.col = threadIdx.x % (D / kPer) * kPer;
+    p.in = r < s.pitch;
+    p.valid = r < s.rows;
+    p.code = s.code_row + run * s.rows + r;
+    p.row = run * s.pitch + r;
+    return p;
 }
 
-struct CkptPtrs {
-    void* x[5];
-};
-
-template <typename E>
-struct Chunk;  // 16 bytes of values
-template <>
-struct Chunk<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4& w, float (&f)[4]) {
-        f[0] = __uint_as_float(w.x);
-        f[1] = __uint_as_float(w.y);
-        f[2] = __uint_as_float(w.z);
-        f[3] = __uint_as_float(w.w);
+__device__ __forceinline__ void load16(const float* x, float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 w = reinterpret_cast<const float4*>(x)[i];
+        f[4 * i] = w.x;
+        f[4 * i + 1] = w.y;
+        f[4 * i + 2] = w.z;
+        f[4 * i + 3] = w.w;
     }
-    static __device__ __forceinline__ float code(float x, float a) { return (float)rint(127.0 * (double)x / (double)a); }
-};
-template <>
-struct Chunk<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(const uint4& w, float (&f)[8]) {
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* x, float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(x)[i];
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+            f[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+            f[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
         }
     }
-    // 127 x would overflow from 2^121 on: there both sides are scaled down first
-    static __device__ __forceinline__ float code(float x, float a) {
-        const float f = a >= 0x1p120f ? 0x1p-8f : 1.f;
-        return rintf(__fdiv_rn(127.f * (x * f), a * f));
+}
+__device__ __forceinline__ void store16(float* x, const float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(x)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* x, const float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(f[8 * i + 2 * j], f[8 * i + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        reinterpret_cast<uint4*>(x)[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-};
+}
 
-// Each thread codes 16 bytes of values; the threads of a group of 32 channels
-// are neighbours in a warp.
+// The codes of 16 values of a group whose largest magnitude is a (finite, > 0),
+// in the low bytes of c. Adding 1.5 * 2^23 rounds to a whole number, ties to
+// even, and leaves it in the low bits.
+__device__ __forceinline__ void codes16(float (&f)[kPer], float a, uint32_t (&c)[kPer], __nv_bfloat16) {
+    if (a < 0x1p-100f) {  // 127 / a stays in range
+        a *= 0x1p60f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] *= 0x1p60f;
+    }
+    const float r = __fdiv_ru(127.f, a);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] = __float_as_uint(fmaf(f[i], r, 12582912.f));
+}
+__device__ __forceinline__ void codes16(float (&f)[kPer], float a, uint32_t (&c)[kPer], float) {
+    const double b = a, r = 1.0 / b, half = 0.5 * b;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const double x = 127.0 * f[i];
+        double q = rint(x * r);
+        const double rem = fma(-q, b, x);
+        if (fabs(rem) == half && ((int)q & 1)) q += rem > 0.0 ? 1.0 : -1.0;
+        c[i] = (uint32_t)(int)q;
+    }
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads)
-ckpt_save_kernel(CkptPtrs src, int8_t* __restrict__ codes, float* __restrict__ scales, Sections sec, int n, int pitch) {
-    constexpr int N = Chunk<E>::N, PER_ROW = D / N, LANES = kCkptGroup / N;
-    const int s = section_of(sec, blockIdx.x);
-    const unsigned long long first = s ? sec.end[s - 1] : 0;
-    const unsigned long long at = (unsigned long long)(blockIdx.x - (s ? sec.block_end[s - 1] : 0)) * kThreads + threadIdx.x;
-    const unsigned long long row = at / PER_ROW;
-    const int x = (int)(at % PER_ROW) * N;
-    const bool in = row < sec.end[s] - first;
-    const unsigned long long from = s < 3 ? row : row / n * pitch + row % n;
-    float f[N];
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (in) w = *reinterpret_cast<const uint4*>(static_cast<const E*>(src.x[s]) + from * D + x);
-    Chunk<E>::unpack(w, f);
+ckpt_save_kernel(const __grid_constant__ Sections sec, int8_t* __restrict__ codes, float* __restrict__ scales) {
+    const Place p = place<D>(sec);
+    float f[kPer] = {};
+    if (p.valid) load16(static_cast<const E*>(p.x) + p.row * D + p.col, f);
     // the largest magnitude by bits: a NaN is above infinity, infinity above all else
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!in) return;
+    for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (!p.valid) return;
     const float a = __uint_as_float(top);
     const bool coded = top > 0 && top < 0x7f800000u;
-    uint32_t packed[N / 4] = {};
-    if (coded) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) packed[i >> 2] |= ((uint32_t)(int)Chunk<E>::code(f[i], a) & 0xffu) << (8 * (i & 3));
-    }
-    const unsigned long long to = first + row;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(codes + to * D + x);
-    if (N == 8)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[N / 4 - 1]);
-    else
-        *dst = packed[0];
-    if (x % kCkptGroup == 0)
-        scales[to * (D / kCkptGroup) + x / kCkptGroup] = coded || top == 0 ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
-}
-
-template <typename E>
-__device__ __forceinline__ void store8(E* p, const float (&f)[8]);
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&f)[8]) {
+    uint32_t c[kPer] = {};
+    if (coded) codes16(f, a, c, E());
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&t);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i)
+        w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+    *reinterpret_cast<uint4*>(codes + p.code * D + p.col) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (p.col % kCkptGroup == 0)
+        scales[(p.code * D + p.col) / kCkptGroup] = coded || top == 0 ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
 }
 
-// Each thread restores 8 values. K and V rows are counted over the pitch: the
-// rows of empty slots get zeros.
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads)
-ckpt_restore_kernel(CkptPtrs dst, const int8_t* __restrict__ codes, const float* __restrict__ scales, Sections sec,
-                    Sections out, int n, int pitch) {
-    const int s = section_of(out, blockIdx.x);
-    if (dst.x[s] == nullptr) return;
-    const unsigned long long at = (unsigned long long)(blockIdx.x - (s ? out.block_end[s - 1] : 0)) * kThreads + threadIdx.x;
-    const unsigned long long row = at / (D / 8);
-    const int x = (int)(at % (D / 8)) * 8;
-    if (row >= out.end[s]) return;
-    unsigned long long from = (s ? sec.end[s - 1] : 0) + row;
-    bool valid = true;
-    if (s >= 3) {
-        const unsigned long long slot = row % pitch;
-        valid = slot < (unsigned long long)n;
-        from = sec.end[s - 1] + row / pitch * n + slot;
-    }
-    float f[8] = {};
-    if (valid) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + from * D + x);
-        const float sc = scales[from * (D / kCkptGroup) + x / kCkptGroup];
+ckpt_restore_kernel(const __grid_constant__ Sections sec, const int8_t* __restrict__ codes, const float* __restrict__ scales) {
+    const Place p = place<D>(sec);
+    if (!p.in || p.x == nullptr) return;
+    float f[kPer] = {};
+    if (p.valid) {
+        const uint4 w = *reinterpret_cast<const uint4*>(codes + p.code * D + p.col);
+        const float sc = scales[(p.code * D + p.col) / kCkptGroup];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)(int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * sc;
+        for (int i = 0; i < kPer; ++i) f[i] = (float)(int8_t)(u[i >> 2] >> (8 * (i & 3))) * sc;
     }
-    store8(static_cast<E*>(dst.x[s]) + row * D + x, f);
+    store16(static_cast<E*>(p.x) + p.row * D + p.col, f);
 }
 
-int blocks_for(unsigned long long rows, int per_row) { return (int)((rows * per_row + kThreads - 1) / kThreads); }
-
-Sections sections(const CkptArgs& a, int per_row) {
-    const unsigned long long rows[5] = {(unsigned long long)a.B * a.Hq * a.T, (unsigned long long)a.B * a.Hkv * a.T,
-                                        (unsigned long long)a.B * a.Hkv * a.T, (unsigned long long)a.B * a.Hkv * a.n,
-                                        (unsigned long long)a.B * a.Hkv * a.n};
-    Sections s;
-    unsigned long long r = 0;
+// The save visits the rows of the record, the restore those of the tensors.
+Sections sections(const CkptArgs& a, bool restore) {
+    const unsigned long long groups = (unsigned long long)a.B * a.Hkv;
+    const unsigned long long per = kThreads * kPer / a.d;
+    void* x[5] = {a.q, a.k, a.v, a.K, a.V};
+    Sections out;
+    unsigned long long row = 0;
     int blk = 0;
     for (int i = 0; i < 5; ++i) {
-        s.end[i] = r += rows[i];
-        s.block_end[i] = blk += blocks_for(rows[i], per_row);
+        Section& s = out.s[i];
+        const bool cache = i >= 3;
+        const unsigned long long outer = cache ? groups : 1;
+        s.x = x[i];
+        s.code_row = row;
+        s.rows = cache ? a.n : (i ? groups : (unsigned long long)a.B * a.Hq) * a.T;
+        s.pitch = cache ? a.pitch : s.rows;
+        const unsigned long long visited = restore ? s.pitch : s.rows;
+        s.blocks = (int)((visited + per - 1) / per);
+        row += outer * s.rows;
+        s.block_end = blk += (int)outer * s.blocks;
     }
-    return s;
+    return out;
 }
-
-CkptPtrs pointers(const CkptArgs& a) { return CkptPtrs{{a.q, a.k, a.v, a.K, a.V}}; }
 
 template <typename E, int D>
 cudaError_t save_typed(const CkptArgs& a) {
-    const Sections sec = sections(a, D / Chunk<E>::N);
-    ckpt_save_kernel<E, D><<<sec.block_end[4], kThreads, 0, a.stream>>>(pointers(a), a.codes, a.scales, sec, a.n, a.pitch);
+    const Sections sec = sections(a, false);
+    ckpt_save_kernel<E, D><<<sec.s[4].block_end, kThreads, 0, a.stream>>>(sec, a.codes, a.scales);
     return cudaGetLastError();
 }
 
 template <typename E, int D>
 cudaError_t restore_typed(const CkptArgs& a) {
-    const Sections sec = sections(a, D / 8);
-    Sections out = sec;  // rows written per section, and its blocks
-    int blk = 0;
-    const unsigned long long rows[5] = {(unsigned long long)a.B * a.Hq * a.T, (unsigned long long)a.B * a.Hkv * a.T,
-                                        (unsigned long long)a.B * a.Hkv * a.T, (unsigned long long)a.B * a.Hkv * a.pitch,
-                                        (unsigned long long)a.B * a.Hkv * a.pitch};
-    for (int i = 0; i < 5; ++i) {
-        out.end[i] = rows[i];
-        out.block_end[i] = blk += blocks_for(rows[i], D / 8);
-    }
-    ckpt_restore_kernel<E, D><<<blk, kThreads, 0, a.stream>>>(pointers(a), a.codes, a.scales, sec, out, a.n, a.pitch);
+    const Sections sec = sections(a, true);
+    ckpt_restore_kernel<E, D><<<sec.s[4].block_end, kThreads, 0, a.stream>>>(sec, a.codes, a.scales);
     return cudaGetLastError();
 }
 

@@ -28,11 +28,14 @@ struct TreeArgs {
     const void* Vc;         // [B,Hkv,C,d]
     void* out;              // [B,Hq,T,d]
     float* lse;             // [B,Hq,T]
+    float* part;            // tensor cores: workspace of tree_part_floats() floats
     WaitBound wb;
     cudaStream_t stream;
     int num_sms;
 };
 cudaError_t launch_tree_simt(const TreeArgs& a);
+cudaError_t launch_tree_tc(const TreeArgs& a);  // bf16
+size_t tree_part_floats(int num_sms, int d);
 
 // 8-bit record of a step's inputs: codes of q, k, v (the chunk) and of the n
 // valid slots of K and V, row after row, then their scales in the same order.

@@ -1,0 +1,628 @@
+// tree_tc.cu -- tensor-core (tcgen05 + TMEM + TMA) attention of a tree of drafted
+// tokens over the cache (bf16; the formulas are tree.cu's).
+//
+// The query rows of a KV head, R = G T of them (row = head-in-group * T + node),
+// are cut into 128-row tiles and the keys into 128-key blocks: the cache's first,
+// the drafted nodes' last. A unit is a pair of tiles with all blocks of its KV
+// head. The blocks of all units form one line that is divided evenly over the
+// SMs, one CTA each, so a CTA works on the end of one unit, whole units, and the
+// start of another; a part of a unit leaves its unnormalised output, maximum and
+// sum in fp32, and tree_combine_kernel merges the parts in order.
+//
+// Per block and tile: S = Q K^T in TMEM; one thread per row takes the row into
+// registers, and writes P = 2^(s - m) back over S as bf16, the A operand of
+// O += P V (also in TMEM). The running maximum m moves, and O is rescaled, only
+// when it grows by more than 2^16. A tile's products wait for its softmax, so two
+// tiles share a CTA and every K and V block: one's products run during the
+// other's softmax. Eleven warps: a TMA loader, an MMA issuer and a softmax
+// warpgroup per tile.
+//
+// A row's visible nodes are a bit mask of its ancestors, built in shared memory by
+// pointer jumping (each round a node takes the mask of the node it points to and
+// points where that one does: 8 rounds for 256 nodes). Keys outside the mask get
+// weight zero; a drafted v with a NaN or an infinity is zeroed in shared memory,
+// because zero times it is not zero, and the rows that see it are set to NaN.
+// Rows past the end of a cache, of the nodes or of a KV head's queries arrive as
+// zeros (3-D tensor maps).
+//
+// P is rounded to bf16, the MMA's operand type; maxima, sums and outputs stay in
+// fp32 until the end.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "operators.h"
+#include "tc.h"
+#include "tc_ptx.cuh"
+
+namespace h2o {
+namespace {
+
+using tc::desc_kmajor_sw128;
+using tc::desc_mnmajor_sw128;
+using tc::ex2;
+using tc::fence_after_sync;
+using tc::fence_before_sync;
+
+// P may exceed 1 by up to 2^16 before the running maximum moves: bf16 has fp32's
+// exponents, and O and the sum are fp32.
+constexpr float kRescale = 16.f;
+constexpr int kUnitRows = 256;
+
+template <int D>
+struct TreeCfg {
+    static constexpr int HALF = 128 * 128;  // 128 rows x 64 bf16
+    static constexpr int TILE = 128 * D * 2;
+    static constexpr int RING = 4;          // K / V slots, loaded K0, V0, K1, V1, ...
+    static constexpr int OFF_Q = 0;         // [2 tiles]
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_MASK = OFF_RING + RING * TILE;                  // [2 tiles][256][8] words
+    static constexpr int OFF_PTR = OFF_MASK + 2 * kTreeMaxT * kTreeMaskWords * 4;  // [2 tiles][256]
+    static constexpr int OFF_BAD = OFF_PTR + 2 * kTreeMaxT * 4;              // [2][4] words
+    static constexpr int OFF_BAR = OFF_BAD + 32;
+    static constexpr int NBAR = 28;
+    static constexpr int SMEM_RAW = OFF_BAR + NBAR * 8 + 16 + 1024;
+    static constexpr int SMEM = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;  // one CTA (512 TMEM columns) per SM
+    static constexpr int THREADS = 352;
+    static constexpr uint32_t IDESC_QK = tc::idesc_bf16_f32(128, 128, false);
+    static constexpr uint32_t IDESC_PV = tc::idesc_bf16_f32(128, D, true);
+};
+static_assert(TreeCfg<128>::SMEM_RAW <= 232448, "tree attention shared memory exceeds the per-CTA limit");
+
+struct TreeParams {
+    int Hkv, T, n, R;   // R: query rows per KV head
+    int pairs;          // units per KV head
+    int nbc, nb;        // cache blocks, blocks per unit
+    long long total;    // blocks of all units
+    float scale_log2;
+    const int32_t* parent;
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;   // [2 CTAs][256][D]
+    float2* part_ml; // [2 CTAs][256]: log2-domain maximum (NaN: the row's node is absent) and sum
+    WaitBound wb;
+};
+
+// First block of CTA c's share of the line.
+__host__ __device__ inline long long share(long long total, int ctas, int c) { return total * c / ctas; }
+// The CTA whose share holds block w.
+__host__ __device__ inline int owner(long long total, int ctas, long long w) { return (int)(((w + 1) * ctas - 1) / total); }
+
+// A CTA's next run of blocks of one unit.
+struct Segment {
+    int bg, m0, rows;   // KV head, first row, rows of the unit
+    int j0, j1;         // blocks
+    bool hasB, whole, first;
+};
+__device__ __forceinline__ Segment segment(const TreeParams& p, long long w, long long w0, long long w1) {
+    Segment s;
+    const int unit = (int)(w / p.nb);
+    s.j0 = (int)(w % p.nb);
+    s.j1 = (int)min((long long)p.nb, s.j0 + (w1 - w));
+    s.bg = unit / p.pairs;
+    s.m0 = unit % p.pairs * kUnitRows;
+    s.rows = min(kUnitRows, p.R - s.m0);
+    s.hasB = s.rows > 128;
+    s.whole = s.j0 == 0 && s.j1 == p.nb;
+    s.first = w == w0;
+    return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kc,
+               const __grid_constant__ CUtensorMap map_vc, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const TreeParams p) {
+    using Cfg = TreeCfg<D>;
+    constexpr int RING = Cfg::RING;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+    uint64_t* q_full = bars;
+    uint64_t* q_empty = bars + 1;              // 2 arrivals: the segment's products have read Q
+    uint64_t* ring_full = bars + 2;            // [RING]
+    uint64_t* ring_empty = ring_full + RING;   // [RING], 2 arrivals
+    uint64_t* s_full = ring_empty + RING;      // [2 tiles]; O of the blocks before is complete too
+    uint64_t* p_full = s_full + 2;             // [2 tiles][2 halves], 4 arrivals
+    uint64_t* o_full = p_full + 4;             // [2 tiles]: O of a segment
+    uint64_t* v_ok = o_full + 2;               // [2], 4 arrivals: a node block's V is finite
+    uint64_t* drain = v_ok + 2;                // [2 tiles]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NBAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long w0 = share(p.total, gridDim.x, blockIdx.x), w1 = share(p.total, gridDim.x, blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 2);
+        for (int s = 0; s < RING; ++s) {
+            mbar_init(ring_full + s, 1);
+            mbar_init(ring_empty + s, 2);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + t, 1);
+            mbar_init(p_full + 2 * t, 4);
+            mbar_init(p_full + 2 * t + 1, 4);
+            mbar_init(o_full + t, 1);
+            mbar_init(v_ok + t, 4);
+            mbar_init(drain + t, 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *tmem_slot;  // tile X: S at 256 X, O at 256 X + 128
+    const uint32_t sbase = smem_u32(smem);
+    griddep_launch_dependents();  // the merge waits for this grid's end before it reads
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ loader
+        if (lane == 0) {
+            int L = 0, q = 0;
+            bool ok = true;
+            for (long long w = w0; ok && w < w1; ++q) {
+                const Segment s = segment(p, w, w0, w1);
+                w += s.j1 - s.j0;
+                if (!(ok = wait_bar(q_empty, (q & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag))) break;
+                mbar_arrive_expect_tx(q_full, Cfg::TILE * (s.hasB ? 2 : 1));
+                for (int x = 0; x < (s.hasB ? 2 : 1); ++x)
+                    for (int hh = 0; hh < D / 64; ++hh)
+                        tc::tma_load_3d(smem + Cfg::OFF_Q + x * Cfg::TILE + hh * Cfg::HALF, &map_q, 64 * hh, s.m0 + 128 * x, s.bg,
+                                        q_full);
+                for (int j = s.j0; ok && j < s.j1; ++j) {
+                    const bool cache = j < p.nbc;
+                    const int row = 128 * (cache ? j : j - p.nbc);
+                    for (int kv = 0; kv < 2; ++kv, ++L) {
+                        const int slot = L % RING;
+                        if (!(ok = wait_bar(ring_empty + slot, ((L / RING) & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag)))
+                            break;
+                        const CUtensorMap* map = kv ? (cache ? &map_vc : &map_v) : (cache ? &map_kc : &map_k);
+                        mbar_arrive_expect_tx(ring_full + slot, Cfg::TILE);
+                        for (int hh = 0; hh < D / 64; ++hh)
+                            tc::tma_load_3d(smem + Cfg::OFF_RING + slot * Cfg::TILE + hh * Cfg::HALF, map, 64 * hh, row, s.bg,
+                                            ring_full + slot);
+                    }
+                }
+                if (!ok) ++q;  // its Q load was issued
+                if (!ok) break;
+            }
+            // every load issued here has landed before the CTA may exit
+            if (q) wait_bar(q_full, (q - 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+            for (int s = 0; s < RING; ++s) {
+                const int uses = L / RING + (s < L % RING ? 1 : 0);
+                if (uses) wait_bar(ring_full + s, (uses - 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+            }
+        }
+    } else if (warp == 1 || warp == 10) {
+        // ---------------------------------------------------------- MMA issuers
+        const int X = warp == 1 ? 0 : 1;
+        const uint32_t tS = tmem + 256 * X, tO = tS + 128;
+        const uint64_t dQ = desc_kmajor_sw128(sbase + Cfg::OFF_Q + X * Cfg::TILE);
+        const uint64_t dRingK = desc_kmajor_sw128(sbase + Cfg::OFF_RING);
+        const uint64_t dRingV = desc_mnmajor_sw128(sbase + Cfg::OFF_RING, Cfg::HALF);
+        int L = 0, q = 0, c = 0, tb = 0;  // ring loads, segments, blocks of this tile, node blocks
+        bool ok = true;
+        for (long long w = w0; ok && w < w1; ++q) {
+            const Segment s = segment(p, w, w0, w1);
+            w += s.j1 - s.j0;
+            // (also by a tile that sits the segment out: the next segment's Q is loaded
+            // once every load of this one has been used, so no barrier is a phase behind)
+            if (!(ok = warp_wait(q_full, q & 1, p.wb, kDevTimeoutTmaWait, abort_flag))) break;
+            if (X == 1 && !s.hasB) {  // tile A's warp releases for both
+                L += 2 * (s.j1 - s.j0);
+                tb += max(0, s.j1 - max(s.j0, p.nbc));
+                continue;
+            }
+            for (int j = s.j0; j < s.j1; ++j, ++c) {
+                int slot = L % RING;
+                if (!(ok = warp_wait(ring_full + slot, (L / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag))) break;
+                ++L;
+                fence_after_sync();
+                // S: the softmax took its last row out before its P was handed over, and
+                // the product that reads that P was issued before
+                const uint64_t dK = dRingK + (uint64_t)((slot * Cfg::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * Cfg::HALF + (kk & 3) * 32) >> 4;
+                    tc::mma_bf16_ss_warp(tS, dQ + off, dK + off, Cfg::IDESC_QK, kk > 0);
+                }
+                tc::mma_commit_warp(s_full + X);
+                tc::mma_commit_warp(ring_empty + slot);
+                if (!s.hasB) tc::mma_commit_warp(ring_empty + slot);
+                slot = L % RING;
+                ok = warp_wait(ring_full + slot, (L / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+                ++L;
+                if (ok && j >= p.nbc) {
+                    ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+                    ++tb;
+                }
+                if (!ok) break;
+                const uint64_t dV = dRingV + (uint64_t)((slot * Cfg::TILE) >> 4);
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok = warp_wait(p_full + 2 * X + h, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = 4 * h + k4;  // 16 keys per instruction
+                        tc::mma_bf16_ts_warp(tO, tS + 8 * kk, dV + (uint64_t)((kk * 16 * 128) >> 4), Cfg::IDESC_PV,
+                                             (j > s.j0 || kk > 0) ? 1u : 0u);
+                    }
+                }
+                if (!ok) break;
+                tc::mma_commit_warp(ring_empty + slot);
+                if (!s.hasB) tc::mma_commit_warp(ring_empty + slot);
+            }
+            if (!ok) break;
+            tc::mma_commit_warp(o_full + X);
+            tc::mma_commit_warp(q_empty);
+            if (!s.hasB) tc::mma_commit_warp(q_empty);
+        }
+        // all MMAs issued here complete before TMEM can be released
+        tc::mma_commit_warp(drain + X);
+        __syncwarp();
+        warp_wait(drain + X, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
+    } else {
+        // -------------------------------------------------------------- softmax
+        // A warp that gives up a wait goes on without waiting: every warp joins every
+        // named barrier.
+        const int X = warp < 6 ? 0 : 1;
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;  // row inside the tile = TMEM lane
+        const uint32_t tS = tmem + 256 * X + ((uint32_t)(quad * 32) << 16), tO = tS + 128;
+        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MASK) + X * kTreeMaxT * kTreeMaskWords;
+        int* ptr = reinterpret_cast<int*>(smem + Cfg::OFF_PTR) + X * kTreeMaxT;
+        uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAD);
+        int L = 0, c = 0, tb = 0, done = 0;  // ring loads, blocks of this tile, node blocks, segments of this tile
+        bool ok = true;
+        for (long long w = w0; w < w1;) {
+            const Segment s = segment(p, w, w0, w1);
+            w += s.j1 - s.j0;
+            const int tree_blocks = max(0, s.j1 - max(s.j0, p.nbc));
+            if (X == 1 && !s.hasB) {
+                L += 2 * (s.j1 - s.j0);
+                tb += tree_blocks;
+                continue;
+            }
+            const int row = s.m0 + 128 * X + r;       // of the KV head
+            const bool row_ok = row < p.R;
+            const bool busy = s.m0 + 128 * X + 32 * quad < p.R;  // the warp has rows
+            const int node = row % p.T;
+            if (tree_blocks) {
+                // masks of all nodes: the tile's 128 threads take two each
+                const int b = s.bg / p.Hkv;
+                uint32_t mw[2][kTreeMaskWords];
+                int to[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int i = r + 128 * u;
+                    to[u] = -2;
+                    if (i < p.T) {
+                        const int up = p.parent[(size_t)b * p.T + i];
+                        to[u] = up == -1 ? -1 : (up >= 0 && up < i) ? up : -2;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kTreeMaskWords; ++k) mw[u][k] = (i >> 5) == k ? 1u << (i & 31) : 0u;
+                }
+                tc::named_sync(1 + X, 128);  // the last segment's masks have been read
+                for (int span = 1;; span *= 2) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int i = r + 128 * u;
+                        ptr[i] = to[u];
+#pragma unroll
+                        for (int k = 0; k < kTreeMaskWords; k += 4)
+                            *reinterpret_cast<uint4*>(mask + i * kTreeMaskWords + k) =
+                                make_uint4(mw[u][k], mw[u][k + 1], mw[u][k + 2], mw[u][k + 3]);
+                    }
+                    tc::named_sync(1 + X, 128);
+                    if (span >= p.T) break;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (to[u] < 0) continue;
+                        const uint4* from = reinterpret_cast<const uint4*>(mask + to[u] * kTreeMaskWords);
+                        const uint4 a = from[0], e = from[1];
+                        mw[u][0] |= a.x;
+                        mw[u][1] |= a.y;
+                        mw[u][2] |= a.z;
+                        mw[u][3] |= a.w;
+                        mw[u][4] |= e.x;
+                        mw[u][5] |= e.y;
+                        mw[u][6] |= e.z;
+                        mw[u][7] |= e.w;
+                        to[u] = ptr[to[u]];
+                    }
+                    tc::named_sync(1 + X, 128);
+                }
+            }
+            const bool absent = tree_blocks && ptr[node] != -1;
+            bool spoilt = false;  // the row sees a drafted v that is not finite
+            float m = -INFINITY, l = 0.f;
+            for (int j = s.j0; j < s.j1; ++j, ++c, L += 2) {
+                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+                bool masked = false;
+                if (j >= p.nbc) {
+                    masked = true;
+                    const uint4 mk = *reinterpret_cast<const uint4*>(mask + node * kTreeMaskWords + 4 * (j - p.nbc));
+                    vis[0] = mk.x;
+                    vis[1] = mk.y;
+                    vis[2] = mk.z;
+                    vis[3] = mk.w;
+                    if (X == 0) {
+                        uint32_t* bw = bad + 4 * (tb & 1);
+                        // V of the nodes: rows that are not finite become zeros
+                        if (r < 4) bw[r] = 0;
+                        tc::named_sync(1, 128);
+                        const int slot = (L + 1) % RING;
+                        if (ok) ok = warp_wait(ring_full + slot, ((L + 1) / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+                        uint8_t* vt = smem + Cfg::OFF_RING + slot * Cfg::TILE + r * 128;
+                        uint32_t over = 0;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (x >> 3) * Cfg::HALF + (((x & 7) ^ (r & 7)) << 4));
+                            const uint32_t u[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                over |= (uint32_t)((u[k] & 0x7f80u) == 0x7f80u) | (uint32_t)((u[k] & 0x7f800000u) == 0x7f800000u);
+                        }
+                        if (over) {
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x)
+                                *reinterpret_cast<uint4*>(vt + (x >> 3) * Cfg::HALF + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            atomicOr(bw + quad, 1u << lane);
+                        }
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v_ok + (tb & 1));
+                    }
+                } else if (p.n - 128 * j < 128) {
+                    masked = true;
+                    const int limit = p.n - 128 * j;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        vis[k] = limit >= 32 * k + 32 ? ~0u : limit <= 32 * k ? 0u : (1u << (limit - 32 * k)) - 1;
+                }
+                if (ok) ok = warp_wait(s_full + X, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+                if (j >= p.nbc) {
+                    if (ok) ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) spoilt |= (vis[k] & bad[4 * (tb & 1) + k]) != 0;
+                    ++tb;
+                }
+                fence_after_sync();
+                if (!busy) {  // P of rows that nobody reads: whatever S holds
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(p_full + 2 * X);
+                        mbar_arrive(p_full + 2 * X + 1);
+                    }
+                    continue;
+                }
+                uint32_t v[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc::reg_fence(v[k]);
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((vis[k] >> e) & 1u)) v[k][e] = __float_as_uint(-INFINITY);
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        mx0 = tc::max3(mx0, __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+                        mx1 = tc::max3(mx1, __uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3]));
+                    }
+                const float m_new = fmaxf(m, fmaxf(mx0, mx1) * p.scale_log2);
+                const bool resc = m_new > m + kRescale;
+                const float m_use = resc ? m_new : m;
+                const float alpha = resc ? ex2(m - m_use) : 1.f;
+                if (j > s.j0 && __any_sync(0xffffffffu, resc)) {
+                    // O of the blocks before is complete: their products were issued before
+                    // this S, and the next one waits for this P
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + 32 * k, o);
+                        tc::tmem_ld_wait();
+                        tc::reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::tmem_st32(tO + 32 * k, o);
+                    }
+                }
+                const float ms = m_use == -INFINITY ? 0.f : m_use;  // the row sees no key yet
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ms, -ms);
+                float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // a NaN or +inf score makes its P and the sum NaN
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float2 x = tc::ffma2(make_float2(__uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1])), sc2, nm2);
+                        const float2 y = tc::ffma2(make_float2(__uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3])), sc2, nm2);
+                        const float2 a = make_float2(ex2(x.x), ex2(x.y)), b = make_float2(ex2(y.x), ex2(y.y));
+                        acc0 = tc::fadd2(acc0, a);
+                        acc1 = tc::fadd2(acc1, b);
+                        pk[e >> 1] = tc::pack_bf16(a.x, a.y);
+                        pk[(e >> 1) + 1] = tc::pack_bf16(b.x, b.y);
+                    }
+                    tc::tmem_st16(tS + 16 * k, pk);
+                    if (k & 1) {
+                        tc::tmem_st_wait();
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full + 2 * X + (k >> 1));
+                    }
+                }
+                l = fmaf(l, alpha, (acc0.x + acc0.y) + (acc1.x + acc1.y));
+                m = m_use;
+            }
+            // ---------------------------------------------------------- epilogue
+            if (ok) ok = warp_wait(o_full + X, done++ & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+            fence_after_sync();
+            if (busy && ok) {
+                const float nan = __uint_as_float(0x7fffffffu);
+                const size_t slot = ((size_t)(2 * blockIdx.x + (s.first ? 0 : 1))) * kUnitRows + 128 * X + r;
+                const size_t at = (size_t)s.bg * p.R + row;
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + 32 * k, o);
+                    tc::tmem_ld_wait();
+                    tc::reg_fence(o);
+                    if (!row_ok) continue;
+                    if (!s.whole) {
+                        float* dst = p.part_o + slot * D + 32 * k;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(dst + e) =
+                                spoilt ? make_float4(nan, nan, nan, nan)
+                                       : make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                                     __uint_as_float(o[e + 3]));
+                    } else {
+                        const float f = spoilt ? nan : inv;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                h[x] = absent ? 0u
+                                              : tc::pack_bf16(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f);
+                            *reinterpret_cast<uint4*>(p.out + at * D + 32 * k + e) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+                if (row_ok) {
+                    if (!s.whole)
+                        p.part_ml[slot] = make_float2(absent ? nan : m, l);
+                    else
+                        p.lse[at] = absent ? -INFINITY : (m + log2f(l)) * kLn2;
+                }
+            }
+            fence_before_sync();
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Merges the parts of the units that were divided, one warp per query row: with
+// the parts' maxima m and sums l, M = max m, L = sum l 2^(m - M),
+// O = sum 2^(m - M) O_part / L, in the order of the parts.
+template <int D>
+__global__ void __launch_bounds__(256)
+tree_combine_kernel(const TreeParams p, int ctas, long long rows) {
+    griddep_wait();
+    const long long g = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (g >= rows) return;  // warp-uniform
+    const int row = (int)(g % p.R);
+    const long long unit = g / p.R * p.pairs + row / kUnitRows;
+    const long long b0 = unit * p.nb, b1 = b0 + p.nb;
+    const int c0 = owner(p.total, ctas, b0), c1 = owner(p.total, ctas, b1 - 1);
+    if (c0 == c1) return;  // written whole
+    // where CTA c left this row
+    auto slot = [&](int c) {
+        const bool first = share(p.total, ctas, c) / p.nb == unit;
+        return (size_t)(2 * c + (first ? 0 : 1)) * kUnitRows + row % kUnitRows;
+    };
+    constexpr int V = D / 32;  // values per lane
+    float M = -INFINITY;
+    bool absent = false;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const float m = p.part_ml[slot(c)].x;
+        absent |= m != m;
+        M = fmaxf(M, m);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    absent = __any_sync(0xffffffffu, absent);
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[V] = {};
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const size_t at = slot(c);
+        const float2 ml = p.part_ml[at];
+        float o[V];
+        if (V == 4)
+            *reinterpret_cast<float4*>(o) = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+        else
+            *reinterpret_cast<float2*>(o) = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
+        const float w = ex2(ml.x - ms);
+        L = fmaf(ml.y, w, L);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(o[k], w, acc[k]);
+    }
+    const float inv = 1.f / L;
+    uint32_t h[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) h[k] = absent ? 0u : tc::pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)g * D) + lane * (V / 2);
+    if (V == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[V / 2 - 1]);
+    else
+        *dst = h[0];
+    if (lane == 0) p.lse[g] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+template <int D>
+cudaError_t tree_launch(const TreeArgs& a) {
+    using Cfg = TreeCfg<D>;
+    if (cudaError_t e = ensure_smem_limit(tree_tc_kernel<D>, Cfg::SMEM); e != cudaSuccess) return e;
+    CUtensorMap mq, mkc, mvc, mk, mv;
+    const uint64_t groups = (uint64_t)a.B * a.Hkv;
+    const int R = a.Hq / a.Hkv * a.T;
+    const uint64_t n = a.n > 0 ? a.n : 1;  // an empty cache is never loaded from
+    if (!tc_make_map3(&mq, a.q, R, groups, R, D, 128) || !tc_make_map3(&mkc, a.Kc, n, groups, a.C, D, 128) ||
+        !tc_make_map3(&mvc, a.Vc, n, groups, a.C, D, 128) || !tc_make_map3(&mk, a.k, a.T, groups, a.T, D, 128) ||
+        !tc_make_map3(&mv, a.v, a.T, groups, a.T, D, 128))
+        return cudaErrorInvalidValue;
+    TreeParams p;
+    p.Hkv = a.Hkv;
+    p.T = a.T;
+    p.n = a.n;
+    p.R = R;
+    p.pairs = (R + kUnitRows - 1) / kUnitRows;
+    p.nbc = (a.n + 127) / 128;
+    p.nb = p.nbc + (a.T + 127) / 128;
+    p.total = (long long)groups * p.pairs * p.nb;
+    p.scale_log2 = kLog2e / sqrtf((float)D);
+    p.parent = a.parent;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.lse = a.lse;
+    p.part_o = a.part;
+    p.part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * a.num_sms * kUnitRows * D);
+    p.wb = a.wb;
+    const int ctas = (int)std::min<long long>(a.num_sms, p.total);
+    cudaError_t e = launch_ex(false, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
+    if (e != cudaSuccess) return e;
+    bool divided = false;
+    for (int c = 1; c < ctas && !divided; ++c) divided = share(p.total, ctas, c) % p.nb != 0;
+    if (!divided) return cudaSuccess;
+    const long long rows = (long long)groups * R;
+    return launch_ex(true, tree_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, a.stream, p, ctas, rows);
+}
+
+}  // namespace
+
+size_t tree_part_floats(int num_sms, int d) { return (size_t)2 * num_sms * kUnitRows * (d + 2); }
+
+cudaError_t launch_tree_tc(const TreeArgs& a) { return a.d == 64 ? tree_launch<64>(a) : tree_launch<128>(a); }
+
+}  // namespace h2o

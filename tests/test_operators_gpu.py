@@ -206,6 +206,25 @@ def test_checkpoint_codes_scales_and_values(dtype, B, Hkv, G, d, C, n, T):
         assert torch.equal(got.isnan(), w.isnan())
 
 
+@pytest.mark.parametrize("exponent", [-120, -40, 0, 100])
+def test_checkpoint_codes_of_every_bf16_quotient(exponent):
+    """Every pair of an 8-bit largest magnitude and an 8-bit value at or below it
+    by up to 2^9, the borders k + 1/2 among them."""
+    top = torch.arange(128, 256, device="cuda", dtype=torch.float64)
+    x = torch.stack([torch.arange(128, 256, device="cuda", dtype=torch.float64) * 2.0**-s for s in range(10)]).reshape(-1)
+    x = torch.cat([x, x.new_zeros(-len(x) % 31)]).view(1, -1, 31)
+    g = torch.cat([top.view(-1, 1, 1).expand(-1, x.shape[1], 1), x.expand(128, -1, -1)], 2)
+    g = torch.where(g > g[..., :1], -g / 2, g) * 2.0**exponent   # nothing above the first
+    rows = g.reshape(-1, 32).to(BF16)
+    rows = torch.cat([rows, rows.new_zeros((-len(rows) % 4, 32))]).view(1, 1, -1, 128)
+    c = H2OCache(1, 1, 1, 128, 4, BF16, max_T=rows.shape[2])
+    ck = c.checkpoint(rows, rows, -rows)
+    want = ref.quantise(rows)
+    for got, sign in zip(ck.codes(), (1, 1, -1)):
+        assert torch.equal(got, want[0] * sign)
+    assert torch.equal(ck.scales()[0], want[1])
+
+
 def test_checkpoint_outlives_the_cache_it_was_taken_from():
     q, k, v, K, V = heads(BF16, 1, 2, 2, 64, 64, 64, 16)
     c = cache_of(K, V, 4, 64)
