@@ -79,7 +79,7 @@ struct TreeParams {
     const int32_t* parent;
     __nv_bfloat16* out;
     float* lse;
-    float* part_o;   // [2 CTAs][256][D]
+    float4* part_o;  // [2 CTAs][D / 4][256]: four columns of a row together, rows next to each other
     float2* part_ml; // [2 CTAs][256]: log2-domain maximum (NaN: the row's node is absent) and sum
     WaitBound wb;
 };
@@ -402,62 +402,70 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                     continue;
                 }
-                uint32_t v[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc::reg_fence(v[k]);
-                if (masked) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                // the row's maximum, then its weights: S is read from TMEM twice, 32 columns
+                // ahead of the arithmetic (holding the whole row spills registers)
+                uint32_t v[2][32];
+                auto take = [&](int k) {  // columns 32 k .. of the row, masked; the next ones on their way
+                    tc::tmem_ld_wait();
+                    tc::reg_fence(v[k & 1]);
+                    if (k < 3) tc::tmem_ld32(tS + 32 * (k + 1), v[(k + 1) & 1]);
+                    if (masked) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((vis[k] >> e) & 1u)) v[k][e] = __float_as_uint(-INFINITY);
-                }
+                            if (!((vis[k] >> e) & 1u)) v[k & 1][e] = __float_as_uint(-INFINITY);
+                    }
+                };
+                tc::tmem_ld32(tS, v[0]);
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {
+                    take(k);
+                    const uint32_t(&s32)[32] = v[k & 1];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        mx0 = tc::max3(mx0, __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
-                        mx1 = tc::max3(mx1, __uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3]));
+                        mx0 = tc::max3(mx0, __uint_as_float(s32[e]), __uint_as_float(s32[e + 1]));
+                        mx1 = tc::max3(mx1, __uint_as_float(s32[e + 2]), __uint_as_float(s32[e + 3]));
                     }
+                }
+                tc::tmem_ld32(tS, v[0]);
                 const float m_new = fmaxf(m, fmaxf(mx0, mx1) * p.scale_log2);
                 const bool resc = m_new > m + kRescale;
                 const float m_use = resc ? m_new : m;
                 const float alpha = resc ? ex2(m - m_use) : 1.f;
-                if (j > s.j0 && __any_sync(0xffffffffu, resc)) {
-                    // O of the blocks before is complete: their products were issued before
-                    // this S, and the next one waits for this P
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(tO + 32 * k, o);
-                        tc::tmem_ld_wait();
-                        tc::reg_fence(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tc::tmem_st32(tO + 32 * k, o);
-                    }
-                }
                 const float ms = m_use == -INFINITY ? 0.f : m_use;  // the row sees no key yet
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ms, -ms);
                 float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {  // a NaN or +inf score makes its P and the sum NaN
+                    take(k);
+                    const uint32_t(&s32)[32] = v[k & 1];
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float2 x = tc::ffma2(make_float2(__uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1])), sc2, nm2);
-                        const float2 y = tc::ffma2(make_float2(__uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3])), sc2, nm2);
+                        const float2 x = tc::ffma2(make_float2(__uint_as_float(s32[e]), __uint_as_float(s32[e + 1])), sc2, nm2);
+                        const float2 y = tc::ffma2(make_float2(__uint_as_float(s32[e + 2]), __uint_as_float(s32[e + 3])), sc2, nm2);
                         const float2 a = make_float2(ex2(x.x), ex2(x.y)), b = make_float2(ex2(y.x), ex2(y.y));
                         acc0 = tc::fadd2(acc0, a);
                         acc1 = tc::fadd2(acc1, b);
                         pk[e >> 1] = tc::pack_bf16(a.x, a.y);
                         pk[(e >> 1) + 1] = tc::pack_bf16(b.x, b.y);
                     }
+                    // over columns that this row has taken (16 k + 15 < 32 k + 32)
                     tc::tmem_st16(tS + 16 * k, pk);
+                    if (k == 1 && j > s.j0 && __any_sync(0xffffffffu, resc)) {
+                        // O of the blocks before is complete: their products were issued before
+                        // this S, and the next one waits for this P
+#pragma unroll
+                        for (int x = 0; x < D / 32; ++x) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(tO + 32 * x, o);
+                            tc::tmem_ld_wait();
+                            tc::reg_fence(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::tmem_st32(tO + 32 * x, o);
+                        }
+                    }
                     if (k & 1) {
                         tc::tmem_st_wait();
                         fence_before_sync();
@@ -473,7 +481,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             fence_after_sync();
             if (busy && ok) {
                 const float nan = __uint_as_float(0x7fffffffu);
-                const size_t slot = ((size_t)(2 * blockIdx.x + (s.first ? 0 : 1))) * kUnitRows + 128 * X + r;
+                const size_t part = 2 * blockIdx.x + (s.first ? 0 : 1);
                 const size_t at = (size_t)s.bg * p.R + row;
                 const float inv = 1.f / l;
 #pragma unroll
@@ -484,10 +492,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     tc::reg_fence(o);
                     if (!row_ok) continue;
                     if (!s.whole) {
-                        float* dst = p.part_o + slot * D + 32 * k;
+                        float4* dst = p.part_o + (part * (D / 4) + 8 * k) * kUnitRows + 128 * X + r;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(dst + e) =
+                            dst[(e >> 2) * kUnitRows] =
                                 spoilt ? make_float4(nan, nan, nan, nan)
                                        : make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                                      __uint_as_float(o[e + 3]));
@@ -506,7 +514,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
                 if (row_ok) {
                     if (!s.whole)
-                        p.part_ml[slot] = make_float2(absent ? nan : m, l);
+                        p.part_ml[part * kUnitRows + 128 * X + r] = make_float2(absent ? nan : m, l);
                     else
                         p.lse[at] = absent ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
@@ -522,63 +530,53 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     }
 }
 
-// Merges the parts of the units that were divided, one warp per query row: with
-// the parts' maxima m and sums l, M = max m, L = sum l 2^(m - M),
-// O = sum 2^(m - M) O_part / L, in the order of the parts.
+// Merges the parts of the units that were divided: with the parts' maxima m and
+// sums l, M = max m, L = sum l 2^(m - M), O = sum 2^(m - M) O_part / L, in the
+// order of the parts. One thread per four columns of a row; a block takes 1024 / D
+// consecutive rows, neighbouring lanes neighbouring rows, as the parts lie.
 template <int D>
 __global__ void __launch_bounds__(256)
-tree_combine_kernel(const TreeParams p, int ctas, long long rows) {
+tree_combine_kernel(const TreeParams p, int ctas, unsigned rows) {
     griddep_wait();
-    const long long g = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (g >= rows) return;  // warp-uniform
-    const int row = (int)(g % p.R);
-    const long long unit = g / p.R * p.pairs + row / kUnitRows;
-    const long long b0 = unit * p.nb, b1 = b0 + p.nb;
-    const int c0 = owner(p.total, ctas, b0), c1 = owner(p.total, ctas, b1 - 1);
+    constexpr unsigned kRows = 1024 / D;
+    const unsigned g = blockIdx.x * kRows + threadIdx.x % kRows;
+    const int col4 = threadIdx.x / kRows;
+    if (g >= rows) return;
+    const int row = (int)(g % (unsigned)p.R);
+    const long long b0 = (long long)(g / (unsigned)p.R * p.pairs + row / kUnitRows) * p.nb;
+    const int c0 = owner(p.total, ctas, b0), c1 = owner(p.total, ctas, b0 + p.nb - 1);
     if (c0 == c1) return;  // written whole
-    // where CTA c left this row
-    auto slot = [&](int c) {
-        const bool first = share(p.total, ctas, c) / p.nb == unit;
-        return (size_t)(2 * c + (first ? 0 : 1)) * kUnitRows + row % kUnitRows;
-    };
-    constexpr int V = D / 32;  // values per lane
+    // where CTA c left its part: the unit is the first one of every CTA but, it may be, c0
+    const bool second = share(p.total, ctas, c0) < b0;
+    auto part = [&](int c) { return (size_t)(2 * c + (c == c0 && second ? 1 : 0)); };
+    const int r = row % kUnitRows;
     float M = -INFINITY;
     bool absent = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float m = p.part_ml[slot(c)].x;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const float m = p.part_ml[part(c) * kUnitRows + r].x;
         absent |= m != m;
         M = fmaxf(M, m);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    absent = __any_sync(0xffffffffu, absent);
     const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[V] = {};
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
-        const size_t at = slot(c);
-        const float2 ml = p.part_ml[at];
-        float o[V];
-        if (V == 4)
-            *reinterpret_cast<float4*>(o) = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
-        else
-            *reinterpret_cast<float2*>(o) = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
+        const float2 ml = p.part_ml[part(c) * kUnitRows + r];
+        const float4 o = p.part_o[(part(c) * (D / 4) + col4) * kUnitRows + r];
         const float w = ex2(ml.x - ms);
         L = fmaf(ml.y, w, L);
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(o[k], w, acc[k]);
+        acc.x = fmaf(o.x, w, acc.x);
+        acc.y = fmaf(o.y, w, acc.y);
+        acc.z = fmaf(o.z, w, acc.z);
+        acc.w = fmaf(o.w, w, acc.w);
     }
     const float inv = 1.f / L;
-    uint32_t h[V / 2];
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) h[k] = absent ? 0u : tc::pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)g * D) + lane * (V / 2);
-    if (V == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[V / 2 - 1]);
-    else
-        *dst = h[0];
-    if (lane == 0) p.lse[g] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
+    uint2 h = make_uint2(tc::pack_bf16(acc.x * inv, acc.y * inv), tc::pack_bf16(acc.z * inv, acc.w * inv));
+    if (absent) h = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(p.out + (size_t)g * D + 4 * col4) = h;
+    if (col4 == 0) p.lse[g] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int D>
@@ -606,7 +604,7 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.parent = a.parent;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
-    p.part_o = a.part;
+    p.part_o = reinterpret_cast<float4*>(a.part);
     p.part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * a.num_sms * kUnitRows * D);
     p.wb = a.wb;
     const int ctas = (int)std::min<long long>(a.num_sms, p.total);
@@ -615,8 +613,8 @@ cudaError_t tree_launch(const TreeArgs& a) {
     bool divided = false;
     for (int c = 1; c < ctas && !divided; ++c) divided = share(p.total, ctas, c) % p.nb != 0;
     if (!divided) return cudaSuccess;
-    const long long rows = (long long)groups * R;
-    return launch_ex(true, tree_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, a.stream, p, ctas, rows);
+    const unsigned rows = (unsigned)(groups * R);  // a [B,Hq,T,d] tensor of 2^32 rows does not fit the card
+    return launch_ex(true, tree_combine_kernel<D>, dim3((rows + 1024 / D - 1) / (1024 / D)), dim3(256), 0, a.stream, p, ctas, rows);
 }
 
 }  // namespace
