@@ -9,13 +9,13 @@
 // start of another; a part of a unit leaves its unnormalised output, maximum and
 // sum in fp32, and tree_combine_kernel merges the parts in order.
 //
-// Per block and tile: S = Q K^T in TMEM; one thread per row takes the row into
-// registers, and writes P = 2^(s - m) back over S as bf16, the A operand of
-// O += P V (also in TMEM). The running maximum m moves, and O is rescaled, only
-// when it grows by more than 2^16. A tile's products wait for its softmax, so two
-// tiles share a CTA and every K and V block: one's products run during the
-// other's softmax. Eleven warps: a TMA loader, an MMA issuer and a softmax
-// warpgroup per tile.
+// Per block and tile: S = Q K^T in TMEM; two threads per row take 64 columns each
+// into registers, exchange their maxima, and write P = 2^(s - m) back over S as
+// bf16, the A operand of O += P V (also in TMEM). The running maximum m moves, and
+// O is rescaled, only when it grows by more than 2^16. A tile's products wait for
+// its softmax, so two tiles share a CTA and every K and V block: one's products
+// run during the other's softmax. Eighteen warps: a TMA loader, an MMA issuer and
+// two softmax warpgroups per tile.
 //
 // A row's visible nodes are a bit mask of its ancestors, built in shared memory by
 // pointer jumping (each round a node takes the mask of the node it points to and
@@ -60,21 +60,29 @@ struct TreeCfg {
     static constexpr int OFF_MASK = OFF_RING + RING * TILE;                  // [2 tiles][256][8] words
     static constexpr int OFF_PTR = OFF_MASK + 2 * kTreeMaxT * kTreeMaskWords * 4;  // [2 tiles][256]
     static constexpr int OFF_BAD = OFF_PTR + 2 * kTreeMaxT * 4;              // [2][4] words
-    static constexpr int OFF_BAR = OFF_BAD + 32;
+    static constexpr int OFF_MAX = OFF_BAD + 32;                             // [2 tiles][2 blocks][2 halves][128] floats
+    static constexpr int OFF_BAR = OFF_MAX + 2 * 2 * 2 * 128 * 4;
     static constexpr int NBAR = 28;
     static constexpr int SMEM_RAW = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr int SMEM = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;  // one CTA (512 TMEM columns) per SM
-    static constexpr int THREADS = 352;
+    static constexpr int THREADS = 576;
     static constexpr uint32_t IDESC_QK = tc::idesc_bf16_f32(128, 128, false);
     static constexpr uint32_t IDESC_PV = tc::idesc_bf16_f32(128, D, true);
 };
 static_assert(TreeCfg<128>::SMEM_RAW <= 232448, "tree attention shared memory exceeds the per-CTA limit");
 
+// CTA c's share of the line: q blocks, one more for the first `extra` CTAs.
+struct Split {
+    int q, extra;
+    __host__ __device__ int first(int c) const { return c * q + (c < extra ? c : extra); }
+    __host__ __device__ int owner(int w) const { return w < extra * (q + 1) ? w / (q + 1) : extra + (w - extra * (q + 1)) / q; }
+};
+
 struct TreeParams {
     int Hkv, T, n, R;   // R: query rows per KV head
     int pairs;          // units per KV head
     int nbc, nb;        // cache blocks, blocks per unit
-    long long total;    // blocks of all units
+    Split split;        // of the blocks of all units
     float scale_log2;
     const int32_t* parent;
     __nv_bfloat16* out;
@@ -84,22 +92,17 @@ struct TreeParams {
     WaitBound wb;
 };
 
-// First block of CTA c's share of the line.
-__host__ __device__ inline long long share(long long total, int ctas, int c) { return total * c / ctas; }
-// The CTA whose share holds block w.
-__host__ __device__ inline int owner(long long total, int ctas, long long w) { return (int)(((w + 1) * ctas - 1) / total); }
-
 // A CTA's next run of blocks of one unit.
 struct Segment {
     int bg, m0, rows;   // KV head, first row, rows of the unit
     int j0, j1;         // blocks
     bool hasB, whole, first;
 };
-__device__ __forceinline__ Segment segment(const TreeParams& p, long long w, long long w0, long long w1) {
+__device__ __forceinline__ Segment segment(const TreeParams& p, int w, int w0, int w1) {
     Segment s;
-    const int unit = (int)(w / p.nb);
-    s.j0 = (int)(w % p.nb);
-    s.j1 = (int)min((long long)p.nb, s.j0 + (w1 - w));
+    const int unit = w / p.nb;
+    s.j0 = w - unit * p.nb;
+    s.j1 = min(p.nb, s.j0 + (w1 - w));
     s.bg = unit / p.pairs;
     s.m0 = unit % p.pairs * kUnitRows;
     s.rows = min(kUnitRows, p.R - s.m0);
@@ -120,35 +123,34 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint8_t* smem = align1024(smem_raw);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
     uint64_t* q_full = bars;
-    uint64_t* q_empty = bars + 1;              // 2 arrivals: the segment's products have read Q
+    uint64_t* q_empty = bars + 1;              // the segment's products have read Q
     uint64_t* ring_full = bars + 2;            // [RING]
-    uint64_t* ring_empty = ring_full + RING;   // [RING], 2 arrivals
+    uint64_t* ring_empty = ring_full + RING;   // [RING]
     uint64_t* s_full = ring_empty + RING;      // [2 tiles]; O of the blocks before is complete too
-    uint64_t* p_full = s_full + 2;             // [2 tiles][2 halves], 4 arrivals
-    uint64_t* o_full = p_full + 4;             // [2 tiles]: O of a segment
+    uint64_t* p_full = s_full + 2;             // [2 tiles], 8 arrivals: P over S, O rescaled
+    uint64_t* o_full = p_full + 2;             // [2 tiles]: O of a segment
     uint64_t* v_ok = o_full + 2;               // [2], 4 arrivals: a node block's V is finite
-    uint64_t* drain = v_ok + 2;                // [2 tiles]
+    uint64_t* drain = v_ok + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long long w0 = share(p.total, gridDim.x, blockIdx.x), w1 = share(p.total, gridDim.x, blockIdx.x + 1);
+    const int w0 = p.split.first(blockIdx.x), w1 = p.split.first(blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 2);
+        mbar_init(q_empty, 1);
         for (int s = 0; s < RING; ++s) {
             mbar_init(ring_full + s, 1);
-            mbar_init(ring_empty + s, 2);
+            mbar_init(ring_empty + s, 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + t, 1);
-            mbar_init(p_full + 2 * t, 4);
-            mbar_init(p_full + 2 * t + 1, 4);
+            mbar_init(p_full + t, 8);
             mbar_init(o_full + t, 1);
             mbar_init(v_ok + t, 4);
-            mbar_init(drain + t, 1);
         }
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -165,7 +167,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         if (lane == 0) {
             int L = 0, q = 0;
             bool ok = true;
-            for (long long w = w0; ok && w < w1; ++q) {
+            for (int w = w0; ok && w < w1; ++q) {
                 const Segment s = segment(p, w, w0, w1);
                 w += s.j1 - s.j0;
                 if (!(ok = wait_bar(q_empty, (q & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag))) break;
@@ -198,88 +200,94 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (uses) wait_bar(ring_full + s, (uses - 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
             }
         }
-    } else if (warp == 1 || warp == 10) {
-        // ---------------------------------------------------------- MMA issuers
-        const int X = warp == 1 ? 0 : 1;
-        const uint32_t tS = tmem + 256 * X, tO = tS + 128;
-        const uint64_t dQ = desc_kmajor_sw128(sbase + Cfg::OFF_Q + X * Cfg::TILE);
+    } else if (warp == 1) {
+        // ----------------------------------------------------------- MMA issuer
+        // One warp for both tiles, so that the tensor core takes a tile's PV(j) and
+        // QK(j + 1) together and then the other's: the two stay out of step, one in its
+        // softmax while the other has the tensor core. With an issuer per tile their
+        // products interleave, both wait and then both take exponentials (98 us at 256
+        // nodes and 16384 slots, against AFTER_US).
+        const uint64_t dQ = desc_kmajor_sw128(sbase + Cfg::OFF_Q);
         const uint64_t dRingK = desc_kmajor_sw128(sbase + Cfg::OFF_RING);
         const uint64_t dRingV = desc_mnmajor_sw128(sbase + Cfg::OFF_RING, Cfg::HALF);
-        int L = 0, q = 0, c = 0, tb = 0;  // ring loads, segments, blocks of this tile, node blocks
+        int L = 0, q = 0, tb = 0, blocks[2] = {0, 0};  // ring loads, segments, node blocks, blocks of a tile
+        auto wait_ring = [&](int& slot) {
+            slot = L % RING;
+            const bool r = warp_wait(ring_full + slot, (L / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+            ++L;
+            return r;
+        };
+        auto issue_qk = [&](int X, int slot) {
+            const uint64_t a = dQ + (uint64_t)((X * Cfg::TILE) >> 4), b = dRingK + (uint64_t)((slot * Cfg::TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * Cfg::HALF + (kk & 3) * 32) >> 4;
+                tc::mma_bf16_ss_warp(tmem + 256 * X, a + off, b + off, Cfg::IDESC_QK, kk > 0);
+            }
+            tc::mma_commit_warp(s_full + X);
+        };
+        auto issue_pv = [&](int X, int slot, bool first) {
+            const uint32_t tS = tmem + 256 * X;
+            const uint64_t b = dRingV + (uint64_t)((slot * Cfg::TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 keys per instruction; the keys' halves at columns 0 and 64
+                tc::mma_bf16_ts_warp(tS + 128, tS + 64 * (kk >> 2) + 8 * (kk & 3), b + (uint64_t)((kk * 16 * 128) >> 4),
+                                     Cfg::IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+        };
         bool ok = true;
-        for (long long w = w0; ok && w < w1; ++q) {
+        for (int w = w0; ok && w < w1; ++q) {
             const Segment s = segment(p, w, w0, w1);
             w += s.j1 - s.j0;
-            // (also by a tile that sits the segment out: the next segment's Q is loaded
-            // once every load of this one has been used, so no barrier is a phase behind)
-            if (!(ok = warp_wait(q_full, q & 1, p.wb, kDevTimeoutTmaWait, abort_flag))) break;
-            if (X == 1 && !s.hasB) {  // tile A's warp releases for both
-                L += 2 * (s.j1 - s.j0);
-                tb += max(0, s.j1 - max(s.j0, p.nbc));
-                continue;
-            }
-            for (int j = s.j0; j < s.j1; ++j, ++c) {
-                int slot = L % RING;
-                if (!(ok = warp_wait(ring_full + slot, (L / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag))) break;
-                ++L;
-                fence_after_sync();
-                // S: the softmax took its last row out before its P was handed over, and
-                // the product that reads that P was issued before
-                const uint64_t dK = dRingK + (uint64_t)((slot * Cfg::TILE) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * Cfg::HALF + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16_ss_warp(tS, dQ + off, dK + off, Cfg::IDESC_QK, kk > 0);
-                }
-                tc::mma_commit_warp(s_full + X);
-                tc::mma_commit_warp(ring_empty + slot);
-                if (!s.hasB) tc::mma_commit_warp(ring_empty + slot);
-                slot = L % RING;
-                ok = warp_wait(ring_full + slot, (L / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
-                ++L;
+            const int tiles = s.hasB ? 2 : 1;
+            int ks = 0, vs = 0;
+            if (!(ok = warp_wait(q_full, q & 1, p.wb, kDevTimeoutTmaWait, abort_flag) && wait_ring(ks))) break;
+            fence_after_sync();
+            for (int X = 0; X < tiles; ++X) issue_qk(X, ks);
+            tc::mma_commit_warp(ring_empty + ks);
+            for (int j = s.j0; j < s.j1; ++j) {
+                const bool more = j + 1 < s.j1;
+                ok = wait_ring(vs);
                 if (ok && j >= p.nbc) {
                     ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
                     ++tb;
                 }
-                if (!ok) break;
-                const uint64_t dV = dRingV + (uint64_t)((slot * Cfg::TILE) >> 4);
-                for (int h = 0; h < 2; ++h) {
-                    if (!(ok = warp_wait(p_full + 2 * X + h, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
+                if (ok && more) ok = wait_ring(ks);
+                for (int X = 0; ok && X < tiles; ++X) {
+                    if (!(ok = warp_wait(p_full + X, blocks[X] & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
+                    ++blocks[X];
                     fence_after_sync();
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {
-                        const int kk = 4 * h + k4;  // 16 keys per instruction
-                        tc::mma_bf16_ts_warp(tO, tS + 8 * kk, dV + (uint64_t)((kk * 16 * 128) >> 4), Cfg::IDESC_PV,
-                                             (j > s.j0 || kk > 0) ? 1u : 0u);
-                    }
+                    issue_pv(X, vs, j == s.j0);
+                    // S: the softmax took its last row out before it handed P over, and the
+                    // product that reads that P is ahead of this one
+                    if (more) issue_qk(X, ks);
+                    else tc::mma_commit_warp(o_full + X);
                 }
                 if (!ok) break;
-                tc::mma_commit_warp(ring_empty + slot);
-                if (!s.hasB) tc::mma_commit_warp(ring_empty + slot);
+                tc::mma_commit_warp(ring_empty + vs);
+                if (more) tc::mma_commit_warp(ring_empty + ks);
             }
-            if (!ok) break;
-            tc::mma_commit_warp(o_full + X);
-            tc::mma_commit_warp(q_empty);
-            if (!s.hasB) tc::mma_commit_warp(q_empty);
+            if (ok) tc::mma_commit_warp(q_empty);
         }
         // all MMAs issued here complete before TMEM can be released
-        tc::mma_commit_warp(drain + X);
+        tc::mma_commit_warp(drain);
         __syncwarp();
-        warp_wait(drain + X, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
+        warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
     } else {
         // -------------------------------------------------------------- softmax
         // A warp that gives up a wait goes on without waiting: every warp joins every
         // named barrier.
-        const int X = warp < 6 ? 0 : 1;
+        const int X = warp < 10 ? 0 : 1, h = (warp - 2) >> 2 & 1;  // tile, half of the columns
         const int quad = warp & 3;
         const int r = quad * 32 + lane;  // row inside the tile = TMEM lane
-        const uint32_t tS = tmem + 256 * X + ((uint32_t)(quad * 32) << 16), tO = tS + 128;
+        const uint32_t tX = tmem + 256 * X + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tS = tX + 64 * h, tO = tX + 128 + h * (D / 2);  // this thread's columns of S (and P) and O
         uint32_t* mask = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MASK) + X * kTreeMaxT * kTreeMaskWords;
         int* ptr = reinterpret_cast<int*>(smem + Cfg::OFF_PTR) + X * kTreeMaxT;
         uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAD);
+        float* xmax = reinterpret_cast<float*>(smem + Cfg::OFF_MAX) + X * 512 + r;
         int L = 0, c = 0, tb = 0, done = 0;  // ring loads, blocks of this tile, node blocks, segments of this tile
         bool ok = true;
-        for (long long w = w0; w < w1;) {
+        for (int w = w0; w < w1;) {
             const Segment s = segment(p, w, w0, w1);
             w += s.j1 - s.j0;
             const int tree_blocks = max(0, s.j1 - max(s.j0, p.nbc));
@@ -288,231 +296,207 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 tb += tree_blocks;
                 continue;
             }
-            const int row = s.m0 + 128 * X + r;       // of the KV head
-            const bool row_ok = row < p.R;
+            const int row = s.m0 + 128 * X + r;                  // of the KV head
             const bool busy = s.m0 + 128 * X + 32 * quad < p.R;  // the warp has rows
             const int node = row % p.T;
+            bool absent = false;
             if (tree_blocks) {
-                // masks of all nodes: the tile's 128 threads take two each
-                const int b = s.bg / p.Hkv;
-                uint32_t mw[2][kTreeMaskWords];
-                int to[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int i = r + 128 * u;
-                    to[u] = -2;
-                    if (i < p.T) {
-                        const int up = p.parent[(size_t)b * p.T + i];
-                        to[u] = up == -1 ? -1 : (up >= 0 && up < i) ? up : -2;
-                    }
-#pragma unroll
-                    for (int k = 0; k < kTreeMaskWords; ++k) mw[u][k] = (i >> 5) == k ? 1u << (i & 31) : 0u;
+                // masks of all nodes, one per thread of the tile
+                const int i = 128 * h + r;
+                uint32_t mw[kTreeMaskWords];
+                int to = -2;
+                if (i < p.T) {
+                    const int up = p.parent[(size_t)(s.bg / p.Hkv) * p.T + i];
+                    to = up == -1 ? -1 : (up >= 0 && up < i) ? up : -2;
                 }
-                tc::named_sync(1 + X, 128);  // the last segment's masks have been read
+#pragma unroll
+                for (int k = 0; k < kTreeMaskWords; ++k) mw[k] = (i >> 5) == k ? 1u << (i & 31) : 0u;
+                uint4* own = reinterpret_cast<uint4*>(mask + i * kTreeMaskWords);
+                tc::named_sync(1 + X, 256);  // the last segment's masks have been read
                 for (int span = 1;; span *= 2) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int i = r + 128 * u;
-                        ptr[i] = to[u];
-#pragma unroll
-                        for (int k = 0; k < kTreeMaskWords; k += 4)
-                            *reinterpret_cast<uint4*>(mask + i * kTreeMaskWords + k) =
-                                make_uint4(mw[u][k], mw[u][k + 1], mw[u][k + 2], mw[u][k + 3]);
-                    }
-                    tc::named_sync(1 + X, 128);
+                    ptr[i] = to;
+                    own[0] = make_uint4(mw[0], mw[1], mw[2], mw[3]);
+                    own[1] = make_uint4(mw[4], mw[5], mw[6], mw[7]);
+                    tc::named_sync(1 + X, 256);
                     if (span >= p.T) break;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (to[u] < 0) continue;
-                        const uint4* from = reinterpret_cast<const uint4*>(mask + to[u] * kTreeMaskWords);
+                    if (to >= 0) {
+                        const uint4* from = reinterpret_cast<const uint4*>(mask + to * kTreeMaskWords);
                         const uint4 a = from[0], e = from[1];
-                        mw[u][0] |= a.x;
-                        mw[u][1] |= a.y;
-                        mw[u][2] |= a.z;
-                        mw[u][3] |= a.w;
-                        mw[u][4] |= e.x;
-                        mw[u][5] |= e.y;
-                        mw[u][6] |= e.z;
-                        mw[u][7] |= e.w;
-                        to[u] = ptr[to[u]];
+                        mw[0] |= a.x;
+                        mw[1] |= a.y;
+                        mw[2] |= a.z;
+                        mw[3] |= a.w;
+                        mw[4] |= e.x;
+                        mw[5] |= e.y;
+                        mw[6] |= e.z;
+                        mw[7] |= e.w;
+                        to = ptr[to];
                     }
-                    tc::named_sync(1 + X, 128);
+                    tc::named_sync(1 + X, 256);
                 }
+                absent = ptr[node] != -1;
             }
-            const bool absent = tree_blocks && ptr[node] != -1;
             bool spoilt = false;  // the row sees a drafted v that is not finite
             float m = -INFINITY, l = 0.f;
             for (int j = s.j0; j < s.j1; ++j, ++c, L += 2) {
-                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-                bool masked = false;
-                if (j >= p.nbc) {
-                    masked = true;
-                    const uint4 mk = *reinterpret_cast<const uint4*>(mask + node * kTreeMaskWords + 4 * (j - p.nbc));
-                    vis[0] = mk.x;
-                    vis[1] = mk.y;
-                    vis[2] = mk.z;
-                    vis[3] = mk.w;
-                    if (X == 0) {
-                        uint32_t* bw = bad + 4 * (tb & 1);
-                        // V of the nodes: rows that are not finite become zeros
-                        if (r < 4) bw[r] = 0;
-                        tc::named_sync(1, 128);
-                        const int slot = (L + 1) % RING;
-                        if (ok) ok = warp_wait(ring_full + slot, ((L + 1) / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
-                        uint8_t* vt = smem + Cfg::OFF_RING + slot * Cfg::TILE + r * 128;
-                        uint32_t over = 0;
+                uint32_t vis[2] = {~0u, ~0u};  // of this thread's columns
+                const bool nodes = j >= p.nbc, masked = nodes || p.n - 128 * j < 128;
+                if (nodes && X == 0 && h == 0) {
+                    // V of the nodes: rows that are not finite become zeros
+                    uint32_t* bw = bad + 4 * (tb & 1);
+                    const int slot = (L + 1) % RING;
+                    if (ok) ok = warp_wait(ring_full + slot, ((L + 1) / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
+                    uint8_t* vt = smem + Cfg::OFF_RING + slot * Cfg::TILE + r * 128;
+                    uint32_t over = 0;
+#pragma unroll 4
+                    for (int x = 0; x < D / 8; ++x) {
+                        const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (x >> 3) * Cfg::HALF + (((x & 7) ^ (r & 7)) << 4));
+                        const uint32_t u[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                        for (int x = 0; x < D / 8; ++x) {
-                            const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (x >> 3) * Cfg::HALF + (((x & 7) ^ (r & 7)) << 4));
-                            const uint32_t u[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                over |= (uint32_t)((u[k] & 0x7f80u) == 0x7f80u) | (uint32_t)((u[k] & 0x7f800000u) == 0x7f800000u);
-                        }
-                        if (over) {
-#pragma unroll
-                            for (int x = 0; x < D / 8; ++x)
-                                *reinterpret_cast<uint4*>(vt + (x >> 3) * Cfg::HALF + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                            atomicOr(bw + quad, 1u << lane);
-                        }
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(v_ok + (tb & 1));
+                        for (int k = 0; k < 4; ++k)
+                            over |= (uint32_t)((u[k] & 0x7f80u) == 0x7f80u) | (uint32_t)((u[k] & 0x7f800000u) == 0x7f800000u);
                     }
-                } else if (p.n - 128 * j < 128) {
-                    masked = true;
-                    const int limit = p.n - 128 * j;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        vis[k] = limit >= 32 * k + 32 ? ~0u : limit <= 32 * k ? 0u : (1u << (limit - 32 * k)) - 1;
+                    if (over) {
+#pragma unroll 1
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(vt + (x >> 3) * Cfg::HALF + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    over = __ballot_sync(0xffffffffu, over != 0);
+                    if (lane == 0) bw[quad] = over;
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_ok + (tb & 1));
                 }
                 if (ok) ok = warp_wait(s_full + X, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
-                if (j >= p.nbc) {
+                if (nodes) {
                     if (ok) ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+                    const uint32_t* mk = mask + node * kTreeMaskWords + 4 * (j - p.nbc);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) spoilt |= (vis[k] & bad[4 * (tb & 1) + k]) != 0;
+                    for (int k = 0; k < 4; ++k) spoilt |= (mk[k] & bad[4 * (tb & 1) + k]) != 0;
+                    vis[0] = mk[2 * h];
+                    vis[1] = mk[2 * h + 1];
                     ++tb;
+                } else if (masked) {
+                    const int limit = p.n - 128 * j - 64 * h;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        vis[k] = limit >= 32 * k + 32 ? ~0u : limit <= 32 * k ? 0u : (1u << (limit - 32 * k)) - 1;
                 }
                 fence_after_sync();
+                float* xm = xmax + (c & 1) * 256;
                 if (!busy) {  // P of rows that nobody reads: whatever S holds
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(p_full + 2 * X);
-                        mbar_arrive(p_full + 2 * X + 1);
-                    }
+                    tc::named_sync(1 + X, 256);
+                    if (lane == 0) mbar_arrive(p_full + X);
                     continue;
                 }
-                // the row's maximum, then its weights: S is read from TMEM twice, 32 columns
-                // ahead of the arithmetic (holding the whole row spills registers)
                 uint32_t v[2][32];
-                auto take = [&](int k) {  // columns 32 k .. of the row, masked; the next ones on their way
-                    tc::tmem_ld_wait();
-                    tc::reg_fence(v[k & 1]);
-                    if (k < 3) tc::tmem_ld32(tS + 32 * (k + 1), v[(k + 1) & 1]);
-                    if (masked) {
+                tc::tmem_ld32(tS, v[0]);
+                tc::tmem_ld32(tS + 32, v[1]);
+                tc::tmem_ld_wait();
+                tc::reg_fence(v[0]);
+                tc::reg_fence(v[1]);
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((vis[k] >> e) & 1u)) v[k & 1][e] = __float_as_uint(-INFINITY);
-                    }
-                };
-                tc::tmem_ld32(tS, v[0]);
+                            if (!((vis[k] >> e) & 1u)) v[k][e] = __float_as_uint(-INFINITY);
+                }
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    take(k);
-                    const uint32_t(&s32)[32] = v[k & 1];
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        mx0 = tc::max3(mx0, __uint_as_float(s32[e]), __uint_as_float(s32[e + 1]));
-                        mx1 = tc::max3(mx1, __uint_as_float(s32[e + 2]), __uint_as_float(s32[e + 3]));
+                        mx0 = tc::max3(mx0, __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+                        mx1 = tc::max3(mx1, __uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3]));
                     }
-                }
-                tc::tmem_ld32(tS, v[0]);
-                const float m_new = fmaxf(m, fmaxf(mx0, mx1) * p.scale_log2);
+                mx0 = fmaxf(mx0, mx1);
+                xm[128 * h] = mx0;
+                tc::named_sync(1 + X, 256);
+                const float m_new = fmaxf(m, fmaxf(mx0, xm[128 - 128 * h]) * p.scale_log2);
                 const bool resc = m_new > m + kRescale;
                 const float m_use = resc ? m_new : m;
                 const float alpha = resc ? ex2(m - m_use) : 1.f;
+                if (j > s.j0 && __any_sync(0xffffffffu, resc)) {
+                    // O of the blocks before is complete: their products were issued before
+                    // this S, and the next one waits for this P
+#pragma unroll 1
+                    for (int x = 0; x < D / 2; x += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + x, o);
+                        tc::tmem_ld_wait();
+                        tc::reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::tmem_st16(tO + x, o);
+                    }
+                }
                 const float ms = m_use == -INFINITY ? 0.f : m_use;  // the row sees no key yet
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ms, -ms);
                 float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // a NaN or +inf score makes its P and the sum NaN
-                    take(k);
-                    const uint32_t(&s32)[32] = v[k & 1];
+                for (int k = 0; k < 2; ++k) {  // a NaN or +inf score makes its P and the sum NaN
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float2 x = tc::ffma2(make_float2(__uint_as_float(s32[e]), __uint_as_float(s32[e + 1])), sc2, nm2);
-                        const float2 y = tc::ffma2(make_float2(__uint_as_float(s32[e + 2]), __uint_as_float(s32[e + 3])), sc2, nm2);
+                        const float2 x = tc::ffma2(make_float2(__uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1])), sc2, nm2);
+                        const float2 y = tc::ffma2(make_float2(__uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3])), sc2, nm2);
                         const float2 a = make_float2(ex2(x.x), ex2(x.y)), b = make_float2(ex2(y.x), ex2(y.y));
                         acc0 = tc::fadd2(acc0, a);
                         acc1 = tc::fadd2(acc1, b);
                         pk[e >> 1] = tc::pack_bf16(a.x, a.y);
                         pk[(e >> 1) + 1] = tc::pack_bf16(b.x, b.y);
                     }
-                    // over columns that this row has taken (16 k + 15 < 32 k + 32)
                     tc::tmem_st16(tS + 16 * k, pk);
-                    if (k == 1 && j > s.j0 && __any_sync(0xffffffffu, resc)) {
-                        // O of the blocks before is complete: their products were issued before
-                        // this S, and the next one waits for this P
-#pragma unroll
-                        for (int x = 0; x < D / 32; ++x) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(tO + 32 * x, o);
-                            tc::tmem_ld_wait();
-                            tc::reg_fence(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tc::tmem_st32(tO + 32 * x, o);
-                        }
-                    }
-                    if (k & 1) {
-                        tc::tmem_st_wait();
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_full + 2 * X + (k >> 1));
-                    }
                 }
+                tc::tmem_st_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + X);
                 l = fmaf(l, alpha, (acc0.x + acc0.y) + (acc1.x + acc1.y));
                 m = m_use;
             }
             // ---------------------------------------------------------- epilogue
+            // the halves' sums meet, in the buffer that the last block's maxima are not in
+            float* xl = xmax + (c & 1) * 256;
+            xl[128 * h] = l;
+            tc::named_sync(1 + X, 256);
+            l += xl[128 - 128 * h];
+            tc::named_sync(1 + X, 256);
             if (ok) ok = warp_wait(o_full + X, done++ & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
             fence_after_sync();
             if (busy && ok) {
                 const float nan = __uint_as_float(0x7fffffffu);
+                const bool row_ok = row < p.R;
                 const size_t part = 2 * blockIdx.x + (s.first ? 0 : 1);
                 const size_t at = (size_t)s.bg * p.R + row;
-                const float inv = 1.f / l;
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(tO + 32 * k, o);
+                const float f = s.whole ? 1.f / l : 1.f;
+#pragma unroll 1
+                for (int x = 0; x < D / 2; x += 16) {
+                    uint32_t o[16];
+                    tc::tmem_ld16(tO + x, o);
                     tc::tmem_ld_wait();
                     tc::reg_fence(o);
                     if (!row_ok) continue;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = spoilt ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * f);
+                    const int col = h * (D / 2) + x;
                     if (!s.whole) {
-                        float4* dst = p.part_o + (part * (D / 4) + 8 * k) * kUnitRows + 128 * X + r;
+                        float4* dst = p.part_o + (part * (D / 4) + col / 4) * kUnitRows + 128 * X + r;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            dst[(e >> 2) * kUnitRows] =
-                                spoilt ? make_float4(nan, nan, nan, nan)
-                                       : make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                                     __uint_as_float(o[e + 3]));
+                        for (int e = 0; e < 16; e += 4)
+                            dst[(e >> 2) * kUnitRows] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                    __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     } else {
-                        const float f = spoilt ? nan : inv;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                h[x] = absent ? 0u
-                                              : tc::pack_bf16(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f);
-                            *reinterpret_cast<uint4*>(p.out + at * D + 32 * k + e) = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = absent ? 0u : tc::pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + col);
+                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 }
-                if (row_ok) {
+                if (row_ok && h == 0) {
                     if (!s.whole)
                         p.part_ml[part * kUnitRows + 128 * X + r] = make_float2(absent ? nan : m, l);
                     else
@@ -536,18 +520,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 // consecutive rows, neighbouring lanes neighbouring rows, as the parts lie.
 template <int D>
 __global__ void __launch_bounds__(256)
-tree_combine_kernel(const TreeParams p, int ctas, unsigned rows) {
+tree_combine_kernel(const TreeParams p, unsigned rows) {
     griddep_wait();
     constexpr unsigned kRows = 1024 / D;
     const unsigned g = blockIdx.x * kRows + threadIdx.x % kRows;
     const int col4 = threadIdx.x / kRows;
     if (g >= rows) return;
     const int row = (int)(g % (unsigned)p.R);
-    const long long b0 = (long long)(g / (unsigned)p.R * p.pairs + row / kUnitRows) * p.nb;
-    const int c0 = owner(p.total, ctas, b0), c1 = owner(p.total, ctas, b0 + p.nb - 1);
+    const int b0 = (int)(g / (unsigned)p.R * p.pairs + row / kUnitRows) * p.nb;
+    const int c0 = p.split.owner(b0), c1 = p.split.owner(b0 + p.nb - 1);
     if (c0 == c1) return;  // written whole
     // where CTA c left its part: the unit is the first one of every CTA but, it may be, c0
-    const bool second = share(p.total, ctas, c0) < b0;
+    const bool second = p.split.first(c0) < b0;
     auto part = [&](int c) { return (size_t)(2 * c + (c == c0 && second ? 1 : 0)); };
     const int r = row % kUnitRows;
     float M = -INFINITY;
@@ -599,7 +583,11 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.pairs = (R + kUnitRows - 1) / kUnitRows;
     p.nbc = (a.n + 127) / 128;
     p.nb = p.nbc + (a.T + 127) / 128;
-    p.total = (long long)groups * p.pairs * p.nb;
+    const long long total = (long long)groups * p.pairs * p.nb;
+    if (total >= 1ll << 31) return cudaErrorInvalidValue;  // a cache of this many blocks does not fit the card
+    const int ctas = (int)std::min<long long>(a.num_sms, total);
+    p.split.q = (int)(total / ctas);
+    p.split.extra = (int)(total % ctas);
     p.scale_log2 = kLog2e / sqrtf((float)D);
     p.parent = a.parent;
     p.out = static_cast<__nv_bfloat16*>(a.out);
@@ -607,14 +595,13 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.part_o = reinterpret_cast<float4*>(a.part);
     p.part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * a.num_sms * kUnitRows * D);
     p.wb = a.wb;
-    const int ctas = (int)std::min<long long>(a.num_sms, p.total);
     cudaError_t e = launch_ex(false, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
     bool divided = false;
-    for (int c = 1; c < ctas && !divided; ++c) divided = share(p.total, ctas, c) % p.nb != 0;
+    for (int c = 1; c < ctas && !divided; ++c) divided = p.split.first(c) % p.nb != 0;
     if (!divided) return cudaSuccess;
     const unsigned rows = (unsigned)(groups * R);  // a [B,Hq,T,d] tensor of 2^32 rows does not fit the card
-    return launch_ex(true, tree_combine_kernel<D>, dim3((rows + 1024 / D - 1) / (1024 / D)), dim3(256), 0, a.stream, p, ctas, rows);
+    return launch_ex(true, tree_combine_kernel<D>, dim3((rows + 1024 / D - 1) / (1024 / D)), dim3(256), 0, a.stream, p, rows);
 }
 
 }  // namespace
