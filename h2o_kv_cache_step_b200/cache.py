@@ -5,7 +5,6 @@ current CUDA stream; every computation happens in the library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -25,6 +24,11 @@ def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _record_bytes(B: int, Hq: int, Hkv: int, d: int, T: int, n: int) -> int:
+    """h2o_checkpoint_bytes."""
+    return B * (Hq * T + 2 * Hkv * T + 2 * Hkv * n) * (d + d // _lib.H2O_CKPT_GROUP * 4)
+
+
 class H2OCheckpoint:
     """A step's inputs in 8 bits: the device record ``H2OCache.checkpoint``
     writes, with the sizes it was written for. ``buffer`` (uint8) holds the
@@ -32,11 +36,9 @@ class H2OCheckpoint:
     in the same order (one per 32 channels)."""
 
     def __init__(self, buffer: torch.Tensor, B: int, Hq: int, Hkv: int, d: int, T: int, n: int):
-        rows = B * (Hq * T + 2 * Hkv * T + 2 * Hkv * n)
-        if (buffer.dtype != torch.uint8 or not buffer.is_cuda or buffer.dim() != 1 or not buffer.is_contiguous()
-                or buffer.numel() != rows * (d + d // _lib.H2O_CKPT_GROUP * 4)):
-            raise ValueError(f"buffer: need a flat contiguous CUDA uint8 tensor of "
-                             f"{rows * (d + d // _lib.H2O_CKPT_GROUP * 4)} bytes, got {buffer.dtype} "
+        nbytes = _record_bytes(B, Hq, Hkv, d, T, n)
+        if buffer.dtype != torch.uint8 or not buffer.is_cuda or buffer.shape != (nbytes,) or not buffer.is_contiguous():
+            raise ValueError(f"buffer: need a flat contiguous CUDA uint8 tensor of {nbytes} bytes, got {buffer.dtype} "
                              f"{tuple(buffer.shape)}")
         self.buffer, self.T, self.n = buffer, T, n
         self.shape = (B, Hq, Hkv, d)
@@ -163,28 +165,32 @@ class H2OCache:
         return dq, dK, dV, dk, dv
 
     # -- operators next to the step -----------------------------------------
-    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> ctypes.c_void_p:
-        if t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous():
+    # (a small call costs as much on the host as on the GPU: pointers and streams go
+    # to the library as plain integers)
+    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> int:
+        if t.dtype is not dtype or not t.is_cuda or t.device != self.device or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return _ptr(t)
+        return t.data_ptr()
 
-    def _on(self, stream, *used):
-        """The stream of a call, its pointer, and its inputs marked as used there
-        where it is not the current one."""
-        cur = torch.cuda.current_stream(self.device)
-        if stream is not None and stream.device != self.device:
+    def _on(self, stream, *used) -> int:
+        """The stream of a call; its inputs are marked as used there where it is
+        not the current one."""
+        current = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if stream is None or stream.cuda_stream == current:
+            return current
+        if stream.device != self.device:
             raise ValueError(f"stream: on {stream.device}, the cache is on {self.device}")
-        if stream is None or stream == cur:
-            return None, ctypes.c_void_p(cur.cuda_stream)
         for t in used:
             if t is not None:
                 t.record_stream(stream)
-        return stream, ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
 
     def _empty(self, stream, dtype: torch.dtype, *shapes):
         """New tensors that belong to the stream of the call."""
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        if stream is None:
+            return [torch.empty(x, dtype=dtype, device=self.device) for x in shapes]
+        with torch.cuda.stream(stream):
             return [torch.empty(x, dtype=dtype, device=self.device) for x in shapes]
 
     def tree_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent: torch.Tensor, stream=None):
@@ -201,10 +207,10 @@ class H2OCache:
                 self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
                 self._need("v", v, self.dtype, B, self.Hkv, T, self.d),
                 self._need("parent", parent, torch.int32, B, T)]
-        s, sp = self._on(stream, q, k, v, parent)
-        (out,) = self._empty(s, self.dtype, (B, self.Hq, T, self.d))
-        (lse,) = self._empty(s, torch.float32, (B, self.Hq, T))
-        self._check(lib().h2o_tree_attend(self._h, *args, _ptr(out), _ptr(lse), T, sp))
+        s = self._on(stream, q, k, v, parent)
+        (out,) = self._empty(stream, self.dtype, q.shape)
+        (lse,) = self._empty(stream, torch.float32, q.shape[:3])
+        self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, s))
         return out, lse
 
     def checkpoint(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> H2OCheckpoint:
@@ -216,28 +222,27 @@ class H2OCache:
         args = [self._need("q", q, self.dtype, B, self.Hq, T, self.d),
                 self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
                 self._need("v", v, self.dtype, B, self.Hkv, T, self.d)]
-        bytes_ = ctypes.c_size_t()
-        self._check(lib().h2o_checkpoint_bytes(self._h, T, n, ctypes.byref(bytes_)))
-        s, sp = self._on(stream, q, k, v)
-        (buf,) = self._empty(s, torch.uint8, (bytes_.value,))
-        self._check(lib().h2o_checkpoint_save(self._h, *args, T, _ptr(buf), bytes_, sp))
+        s = self._on(stream, q, k, v)
+        nbytes = _record_bytes(B, self.Hq, self.Hkv, self.d, T, n)
+        (buf,) = self._empty(stream, torch.uint8, (nbytes,))
+        self._check(lib().h2o_checkpoint_save(self._h, *args, T, buf.data_ptr(), nbytes, s))
         return H2OCheckpoint(buf, B, self.Hq, self.Hkv, self.d, T, n)
 
     def _record(self, ck: H2OCheckpoint):
         if ck.shape != (self.B, self.Hq, self.Hkv, self.d) or ck.buffer.device != self.device:
             raise ValueError(f"checkpoint: of {ck.shape} on {ck.buffer.device}, the cache is "
                              f"{(self.B, self.Hq, self.Hkv, self.d)} on {self.device}")
-        return _ptr(ck.buffer), ck.nbytes, ck.T, ck.n
+        return ck.buffer.data_ptr(), ck.nbytes, ck.T, ck.n
 
     def checkpoint_restore(self, ck: H2OCheckpoint, stream=None):
         """The values a checkpoint stands for: (q, k, v, K, V), K and V over all
         C slots with zeros in the empty ones. The cache itself is not changed."""
         rec = self._record(ck)
-        s, sp = self._on(stream, ck.buffer)
-        q, k, v, K, V = self._empty(s, self.dtype, (self.B, self.Hq, ck.T, self.d),
-                                    *[(self.B, self.Hkv, x, self.d) for x in (ck.T, ck.T, self.C, self.C)])
-        self._check(lib().h2o_checkpoint_restore(self._h, *rec, _ptr(q), _ptr(k), _ptr(v), _ptr(K), _ptr(V), sp))
-        return q, k, v, K, V
+        s = self._on(stream, ck.buffer)
+        chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
+        x = self._empty(stream, self.dtype, (self.B, self.Hq, ck.T, self.d), chunk, chunk, cache, cache)
+        self._check(lib().h2o_checkpoint_restore(self._h, *rec, *[t.data_ptr() for t in x], s))
+        return tuple(x)
 
     def checkpoint_backward(self, ck: H2OCheckpoint, dout: torch.Tensor, stream=None):
         """Gradients of the checkpointed step's attention at the values the
@@ -245,10 +250,10 @@ class H2OCache:
         dV over the C slots. The cache itself is not read."""
         rec = self._record(ck)
         do = self._need("dout", dout, self.dtype, self.B, self.Hq, ck.T, self.d)
-        s, sp = self._on(stream, ck.buffer, dout)
-        g = self._empty(s, self.dtype, (self.B, self.Hq, ck.T, self.d),
-                        *[(self.B, self.Hkv, x, self.d) for x in (self.C, self.C, ck.T, ck.T)])
-        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, *[_ptr(t) for t in g], sp))
+        s = self._on(stream, ck.buffer, dout)
+        chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
+        g = self._empty(stream, self.dtype, dout.shape, cache, cache, chunk, chunk)
+        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, *[t.data_ptr() for t in g], s))
         return tuple(g)
 
     def carry_grad(self, token_slots: torch.Tensor, n: int, dK: torch.Tensor, dV: torch.Tensor, dk: torch.Tensor,
@@ -269,11 +274,10 @@ class H2OCache:
                 self._need("dk", dk, self.dtype, *chunk), self._need("dv", dv, self.dtype, *chunk)]
         for name, t in (("gK_next", gK_next), ("gV_next", gV_next)):
             args.append(None if t is None else self._need(name, t, torch.float32, *cache))
-        s, sp = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
-        gK, gV = self._empty(s, torch.float32, cache, cache)
-        gk, gv = self._empty(s, self.dtype, chunk, chunk)
-        self._check(lib().h2o_carry_grad(self._h, *args, _ptr(gK), _ptr(gV), _ptr(gk), _ptr(gv), sp))
-        return gK, gV, gk, gv
+        s = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
+        g = self._empty(stream, torch.float32, cache, cache) + self._empty(stream, self.dtype, chunk, chunk)
+        self._check(lib().h2o_carry_grad(self._h, *args, *[t.data_ptr() for t in g], s))
+        return tuple(g)
 
     def set_policy(self, policy: int) -> None:
         """Eviction ranking for the following steps: _lib.H2O_POLICY_SUM (the

@@ -14,12 +14,13 @@
 // bf16, the A operand of O += P V (also in TMEM). The running maximum m moves, and
 // O is rescaled, only when it grows by more than 2^16. A tile's products wait for
 // its softmax, so two tiles share a CTA and every K and V block: one's products
-// run during the other's softmax. Eighteen warps: a TMA loader, an MMA issuer and
-// two softmax warpgroups per tile.
+// run during the other's softmax. Twenty warps: a TMA loader, an MMA issuer, two
+// softmax warpgroups per tile and two warps for the masks.
 //
 // A row's visible nodes are a bit mask of its ancestors, built in shared memory by
 // pointer jumping (each round a node takes the mask of the node it points to and
-// points where that one does: 8 rounds for 256 nodes). Keys outside the mask get
+// points where that one does: 8 rounds for 256 nodes), by warps of their own while
+// the cache's blocks are worked on. Keys outside the mask get
 // weight zero; a drafted v with a NaN or an infinity is zeroed in shared memory,
 // because zero times it is not zero, and the rows that see it are set to NaN.
 // Rows past the end of a cache, of the nodes or of a KV head's queries arrive as
@@ -57,25 +58,32 @@ struct TreeCfg {
     static constexpr int RING = 4;          // K / V slots, loaded K0, V0, K1, V1, ...
     static constexpr int OFF_Q = 0;         // [2 tiles]
     static constexpr int OFF_RING = 2 * TILE;
-    static constexpr int OFF_MASK = OFF_RING + RING * TILE;                  // [2 tiles][256][8] words
-    static constexpr int OFF_PTR = OFF_MASK + 2 * kTreeMaxT * kTreeMaskWords * 4;  // [2 tiles][256]
-    static constexpr int OFF_BAD = OFF_PTR + 2 * kTreeMaxT * 4;              // [2][4] words
+    static constexpr int OFF_MASK = OFF_RING + RING * TILE;                  // [256][8] words
+    static constexpr int OFF_PTR = OFF_MASK + kTreeMaxT * kTreeMaskWords * 4;  // [256]
+    static constexpr int OFF_BAD = OFF_PTR + kTreeMaxT * 4;              // [2][4] words
     static constexpr int OFF_MAX = OFF_BAD + 32;                             // [2 tiles][2 blocks][2 halves][128] floats
     static constexpr int OFF_BAR = OFF_MAX + 2 * 2 * 2 * 128 * 4;
     static constexpr int NBAR = 28;
     static constexpr int SMEM_RAW = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr int SMEM = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;  // one CTA (512 TMEM columns) per SM
-    static constexpr int THREADS = 576;
+    static constexpr int THREADS = 640;
     static constexpr uint32_t IDESC_QK = tc::idesc_bf16_f32(128, 128, false);
     static constexpr uint32_t IDESC_PV = tc::idesc_bf16_f32(128, D, true);
 };
 static_assert(TreeCfg<128>::SMEM_RAW <= 232448, "tree attention shared memory exceeds the per-CTA limit");
 
-// CTA c's share of the line: q blocks, one more for the first `extra` CTAs.
+// CTA c's share of the line: runs of `run` blocks (the whole line, or one unit) are
+// divided among k CTAs each, q blocks a CTA, one more for the first `extra`.
 struct Split {
-    int q, extra;
-    __host__ __device__ int first(int c) const { return c * q + (c < extra ? c : extra); }
-    __host__ __device__ int owner(int w) const { return w < extra * (q + 1) ? w / (q + 1) : extra + (w - extra * (q + 1)) / q; }
+    int run, k, q, extra;
+    __host__ __device__ int first(int c) const {
+        const int i = c % k;
+        return c / k * run + i * q + (i < extra ? i : extra);
+    }
+    __host__ __device__ int owner(int w) const {
+        const int r = w % run, big = extra * (q + 1);
+        return w / run * k + (r < big ? r / (q + 1) : extra + (r - big) / q);
+    }
 };
 
 struct TreeParams {
@@ -130,7 +138,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint64_t* p_full = s_full + 2;             // [2 tiles], 8 arrivals: P over S, O rescaled
     uint64_t* o_full = p_full + 2;             // [2 tiles]: O of a segment
     uint64_t* v_ok = o_full + 2;               // [2], 4 arrivals: a node block's V is finite
-    uint64_t* drain = v_ok + 2;
+    uint64_t* mask_full = v_ok + 2;            // 2 arrivals: the masks of a segment's nodes
+    uint64_t* mask_free = mask_full + 1;       // 16 arrivals: no longer needed
+    uint64_t* drain = mask_free + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -150,6 +160,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             mbar_init(o_full + t, 1);
             mbar_init(v_ok + t, 4);
         }
+        mbar_init(mask_full, 2);
+        mbar_init(mask_free, 16);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -272,6 +284,65 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tc::mma_commit_warp(drain);
         __syncwarp();
         warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
+    } else if (warp >= 18) {
+        // ------------------------------------------------------------ node masks
+        // (a give-up goes on without waiting: both warps join every barrier)
+        const int t = threadIdx.x - 18 * 32;  // nodes t, t + 64, t + 128, t + 192
+        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MASK);
+        int* ptr = reinterpret_cast<int*>(smem + Cfg::OFF_PTR);
+        int built = 0;
+        bool ok = true;
+        for (int w = w0; w < w1;) {
+            const Segment s = segment(p, w, w0, w1);
+            w += s.j1 - s.j0;
+            if (s.j1 <= p.nbc) continue;
+            uint32_t mw[4][kTreeMaskWords];
+            int to[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = t + 64 * u;
+                to[u] = -2;
+                if (i < p.T) {
+                    const int up = p.parent[(size_t)(s.bg / p.Hkv) * p.T + i];
+                    to[u] = up == -1 ? -1 : (up >= 0 && up < i) ? up : -2;
+                }
+#pragma unroll
+                for (int k = 0; k < kTreeMaskWords; ++k) mw[u][k] = (i >> 5) == k ? 1u << (i & 31) : 0u;
+            }
+            if (ok) ok = warp_wait(mask_free, (built & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag);
+            ++built;
+            for (int span = 1;; span *= 2) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = t + 64 * u;
+                    if (i >= p.T) continue;
+                    ptr[i] = to[u];
+                    uint4* own = reinterpret_cast<uint4*>(mask + i * kTreeMaskWords);
+                    own[0] = make_uint4(mw[u][0], mw[u][1], mw[u][2], mw[u][3]);
+                    own[1] = make_uint4(mw[u][4], mw[u][5], mw[u][6], mw[u][7]);
+                }
+                tc::named_sync(3, 64);
+                if (span >= p.T) break;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (to[u] < 0) continue;
+                    const uint4* from = reinterpret_cast<const uint4*>(mask + to[u] * kTreeMaskWords);
+                    const uint4 a = from[0], e = from[1];
+                    mw[u][0] |= a.x;
+                    mw[u][1] |= a.y;
+                    mw[u][2] |= a.z;
+                    mw[u][3] |= a.w;
+                    mw[u][4] |= e.x;
+                    mw[u][5] |= e.y;
+                    mw[u][6] |= e.z;
+                    mw[u][7] |= e.w;
+                    to[u] = ptr[to[u]];
+                }
+                tc::named_sync(3, 64);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(mask_full);
+        }
     } else {
         // -------------------------------------------------------------- softmax
         // A warp that gives up a wait goes on without waiting: every warp joins every
@@ -281,11 +352,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int r = quad * 32 + lane;  // row inside the tile = TMEM lane
         const uint32_t tX = tmem + 256 * X + ((uint32_t)(quad * 32) << 16);
         const uint32_t tS = tX + 64 * h, tO = tX + 128 + h * (D / 2);  // this thread's columns of S (and P) and O
-        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MASK) + X * kTreeMaxT * kTreeMaskWords;
-        int* ptr = reinterpret_cast<int*>(smem + Cfg::OFF_PTR) + X * kTreeMaxT;
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_MASK);
+        const int* ptr = reinterpret_cast<const int*>(smem + Cfg::OFF_PTR);
         uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAD);
         float* xmax = reinterpret_cast<float*>(smem + Cfg::OFF_MAX) + X * 512 + r;
-        int L = 0, c = 0, tb = 0, done = 0;  // ring loads, blocks of this tile, node blocks, segments of this tile
+        int L = 0, c = 0, tb = 0, done = 0, masks = 0;  // ring loads, blocks of this tile, node blocks, segments of this tile, with nodes
         bool ok = true;
         for (int w = w0; w < w1;) {
             const Segment s = segment(p, w, w0, w1);
@@ -294,48 +365,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (X == 1 && !s.hasB) {
                 L += 2 * (s.j1 - s.j0);
                 tb += tree_blocks;
+                masks += tree_blocks > 0;
                 continue;
             }
             const int row = s.m0 + 128 * X + r;                  // of the KV head
             const bool busy = s.m0 + 128 * X + 32 * quad < p.R;  // the warp has rows
             const int node = row % p.T;
             bool absent = false;
-            if (tree_blocks) {
-                // masks of all nodes, one per thread of the tile
-                const int i = 128 * h + r;
-                uint32_t mw[kTreeMaskWords];
-                int to = -2;
-                if (i < p.T) {
-                    const int up = p.parent[(size_t)(s.bg / p.Hkv) * p.T + i];
-                    to = up == -1 ? -1 : (up >= 0 && up < i) ? up : -2;
-                }
-#pragma unroll
-                for (int k = 0; k < kTreeMaskWords; ++k) mw[k] = (i >> 5) == k ? 1u << (i & 31) : 0u;
-                uint4* own = reinterpret_cast<uint4*>(mask + i * kTreeMaskWords);
-                tc::named_sync(1 + X, 256);  // the last segment's masks have been read
-                for (int span = 1;; span *= 2) {
-                    ptr[i] = to;
-                    own[0] = make_uint4(mw[0], mw[1], mw[2], mw[3]);
-                    own[1] = make_uint4(mw[4], mw[5], mw[6], mw[7]);
-                    tc::named_sync(1 + X, 256);
-                    if (span >= p.T) break;
-                    if (to >= 0) {
-                        const uint4* from = reinterpret_cast<const uint4*>(mask + to * kTreeMaskWords);
-                        const uint4 a = from[0], e = from[1];
-                        mw[0] |= a.x;
-                        mw[1] |= a.y;
-                        mw[2] |= a.z;
-                        mw[3] |= a.w;
-                        mw[4] |= e.x;
-                        mw[5] |= e.y;
-                        mw[6] |= e.z;
-                        mw[7] |= e.w;
-                        to = ptr[to];
-                    }
-                    tc::named_sync(1 + X, 256);
-                }
-                absent = ptr[node] != -1;
-            }
             bool spoilt = false;  // the row sees a drafted v that is not finite
             float m = -INFINITY, l = 0.f;
             for (int j = s.j0; j < s.j1; ++j, ++c, L += 2) {
@@ -370,6 +406,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (ok) ok = warp_wait(s_full + X, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
                 if (nodes) {
                     if (ok) ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+                    if (ok) ok = warp_wait(mask_full, masks & 1, p.wb, kDevTimeoutSlotWait, abort_flag);
+                    absent = ptr[node] != -1;
                     const uint32_t* mk = mask + node * kTreeMaskWords + 4 * (j - p.nbc);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) spoilt |= (mk[k] & bad[4 * (tb & 1) + k]) != 0;
@@ -455,6 +493,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (lane == 0) mbar_arrive(p_full + X);
                 l = fmaf(l, alpha, (acc0.x + acc0.y) + (acc1.x + acc1.y));
                 m = m_use;
+            }
+            if (tree_blocks) {
+                ++masks;
+                __syncwarp();
+                if (lane == 0) {  // for the tile that sits out, too
+                    mbar_arrive(mask_free);
+                    if (!s.hasB) mbar_arrive(mask_free);
+                }
             }
             // ---------------------------------------------------------- epilogue
             // the halves' sums meet, in the buffer that the last block's maxima are not in
@@ -585,9 +631,20 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.nb = p.nbc + (a.T + 127) / 128;
     const long long total = (long long)groups * p.pairs * p.nb;
     if (total >= 1ll << 31) return cudaErrorInvalidValue;  // a cache of this many blocks does not fit the card
-    const int ctas = (int)std::min<long long>(a.num_sms, total);
-    p.split.q = (int)(total / ctas);
-    p.split.extra = (int)(total % ctas);
+    // The line is divided evenly, or every unit among the same number of CTAs: then
+    // fewer CTAs may work, but each leaves one part where most leave two. A part
+    // costs about as much as kPartBlocks blocks (its stores, and the merge of it).
+    // Measured, T=61 B=4 C=4096: EVEN_US us divided evenly, UNIT_US by unit; T=256
+    // C=16384: EVEN2_US and UNIT2_US.
+    constexpr int kPartBlocks = 2;
+    const int units = (int)(total / p.nb), k = std::min(a.num_sms / units, p.nb);
+    const int even = (int)((total + a.num_sms - 1) / a.num_sms) + 2 * kPartBlocks;
+    const bool by_unit = k >= 1 && (p.nb + k - 1) / k + kPartBlocks <= even;
+    const int ctas = by_unit ? units * k : (int)std::min<long long>(a.num_sms, total);
+    p.split.run = by_unit ? p.nb : (int)total;
+    p.split.k = by_unit ? k : ctas;
+    p.split.q = p.split.run / p.split.k;
+    p.split.extra = p.split.run % p.split.k;
     p.scale_log2 = kLog2e / sqrtf((float)D);
     p.parent = a.parent;
     p.out = static_cast<__nv_bfloat16*>(a.out);
