@@ -189,9 +189,16 @@ class H2OCache:
     def _empty(self, stream, dtype: torch.dtype, *shapes):
         """New tensors that belong to the stream of the call."""
         if stream is None:
-            return [torch.empty(x, dtype=dtype, device=self.device) for x in shapes]
+            return [torch.empty(*x, dtype=dtype, device=self.device) for x in shapes]
         with torch.cuda.stream(stream):
-            return [torch.empty(x, dtype=dtype, device=self.device) for x in shapes]
+            return [torch.empty(*x, dtype=dtype, device=self.device) for x in shapes]
+
+    def _like(self, stream, *tensors: torch.Tensor):
+        """As _empty, of the types and shapes of (contiguous) tensors."""
+        if stream is None:
+            return [torch.empty_like(t) for t in tensors]
+        with torch.cuda.stream(stream):
+            return [torch.empty_like(t) for t in tensors]
 
     def tree_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent: torch.Tensor, stream=None):
         """Attention of a tree of T drafted tokens per sequence over the cache,
@@ -208,7 +215,7 @@ class H2OCache:
                 self._need("v", v, self.dtype, B, self.Hkv, T, self.d),
                 self._need("parent", parent, torch.int32, B, T)]
         s = self._on(stream, q, k, v, parent)
-        (out,) = self._empty(stream, self.dtype, q.shape)
+        (out,) = self._like(stream, q)
         (lse,) = self._empty(stream, torch.float32, q.shape[:3])
         self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, s))
         return out, lse
@@ -252,7 +259,7 @@ class H2OCache:
         do = self._need("dout", dout, self.dtype, self.B, self.Hq, ck.T, self.d)
         s = self._on(stream, ck.buffer, dout)
         chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
-        g = self._empty(stream, self.dtype, dout.shape, cache, cache, chunk, chunk)
+        g = self._like(stream, dout) + self._empty(stream, self.dtype, cache, cache, chunk, chunk)
         self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, *[t.data_ptr() for t in g], s))
         return tuple(g)
 
@@ -275,7 +282,8 @@ class H2OCache:
         for name, t in (("gK_next", gK_next), ("gV_next", gV_next)):
             args.append(None if t is None else self._need(name, t, torch.float32, *cache))
         s = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
-        g = self._empty(stream, torch.float32, cache, cache) + self._empty(stream, self.dtype, chunk, chunk)
+        g = (self._empty(stream, torch.float32, cache, cache) if gK_next is None else self._like(stream, gK_next, gK_next)) \
+            + self._like(stream, dk, dv)
         self._check(lib().h2o_carry_grad(self._h, *args, *[t.data_ptr() for t in g], s))
         return tuple(g)
 

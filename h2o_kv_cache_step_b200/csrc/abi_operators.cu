@@ -106,6 +106,12 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     if (c->use_tc && !c->tree_part) {
         if (capturing((cudaStream_t)stream))
             return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
+        const size_t words = (size_t)c->B * c->Hkv;
+        if (!c->tree_count) {
+            H2O_TRY(c, cudaMalloc(&c->tree_count, sizeof(unsigned) * words), "cudaMalloc(tree workspace)");
+            H2O_TRY(c, cudaMemset(c->tree_count, 0, sizeof(unsigned) * words), "cudaMemset(tree workspace)");
+            H2O_TRY(c, cudaStreamSynchronize(nullptr), "cudaMemset(tree workspace)");
+        }
         H2O_TRY(c, cudaMalloc(&c->tree_part, sizeof(float) * tree_part_floats(c->num_sms, c->d)), "cudaMalloc(tree workspace)");
     }
     TreeArgs a{};
@@ -126,6 +132,7 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     a.out = out;
     a.lse = lse;
     a.part = c->tree_part;
+    a.count = c->tree_count;
     a.wb.err_word = c->err_dev;
     a.wb.ns = c->wait_ns;
     a.stream = (cudaStream_t)stream;

@@ -75,6 +75,7 @@ struct h2o_ctx {
     // outgrown one is kept until the context goes, because a captured graph
     // may hold its address)
     float* tree_part = nullptr;
+    unsigned* tree_count = nullptr;
     void* ckpt_ws = nullptr;
     size_t ckpt_ws_bytes = 0;
     std::vector<void*> retired;

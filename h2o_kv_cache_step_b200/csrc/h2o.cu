@@ -228,6 +228,7 @@ int h2o_destroy(h2o_ctx* c) {
     cudaFree(c->Vc);
     cudaFree(c->bwd_rows);
     cudaFree(c->tree_part);
+    cudaFree(c->tree_count);
     cudaFree(c->ckpt_ws);
     for (void* p : c->retired) cudaFree(p);
     cudaFree(c->sdpa_part);

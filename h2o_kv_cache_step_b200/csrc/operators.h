@@ -29,6 +29,7 @@ struct TreeArgs {
     void* out;              // [B,Hq,T,d]
     float* lse;             // [B,Hq,T]
     float* part;            // tensor cores: workspace of tree_part_floats() floats
+    unsigned* count;        // tensor cores: workspace of B * Hkv words, zero between calls
     WaitBound wb;
     cudaStream_t stream;
     int num_sms;

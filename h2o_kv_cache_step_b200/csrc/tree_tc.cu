@@ -96,6 +96,7 @@ struct TreeParams {
     __nv_bfloat16* out;
     float* lse;
     float4* part_o;  // [2 CTAs][D / 4][256]: four columns of a row together, rows next to each other
+    unsigned* count; // [KV heads], zero: CTAs that have left their part (nullptr: merged by a kernel of its own)
     float2* part_ml; // [2 CTAs][256]: log2-domain maximum (NaN: the row's node is absent) and sum
     WaitBound wb;
 };
@@ -118,6 +119,60 @@ __device__ __forceinline__ Segment segment(const TreeParams& p, int w, int w0, i
     s.whole = s.j0 == 0 && s.j1 == p.nb;
     s.first = w == w0;
     return s;
+}
+
+// Four columns of a row of KV head bg from the parts that the CTAs left: with the
+// parts' maxima m and sums l, M = max m, L = sum l 2^(m - M),
+// O = sum 2^(m - M) O_part / L, in the order of the parts.
+template <int D>
+__device__ __forceinline__ void merge_row(const TreeParams& p, unsigned bg, int row, int col4) {
+    const int b0 = (int)(bg * p.pairs + row / kUnitRows) * p.nb;
+    const int c0 = p.split.owner(b0), c1 = p.split.owner(b0 + p.nb - 1);
+    if (c0 == c1) return;  // written whole
+    // where CTA c left its part: the unit is the first one of every CTA but, it may be, c0
+    const bool second = p.split.first(c0) < b0;
+    auto part = [&](int c) { return (size_t)(2 * c + (c == c0 && second ? 1 : 0)); };
+    const int r = row % kUnitRows;
+    constexpr int kBatch = 8;  // parts in flight: one after the other they cost an L2 latency each
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool absent = false;
+    for (int c = c0; c <= c1; c += kBatch) {
+        float2 ml[kBatch];
+        float4 o[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const size_t at = part(min(c + u, c1));
+            ml[u] = p.part_ml[at * kUnitRows + r];
+            o[u] = p.part_o[(at * (D / 4) + col4) * kUnitRows + r];
+        }
+        float Mn = M;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            absent |= ml[u].x != ml[u].x;
+            Mn = fmaxf(Mn, ml[u].x);
+        }
+        const float ms = Mn == -INFINITY ? 0.f : Mn, a = ex2(M - ms);
+        M = Mn;
+        L *= a;
+        acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (c + u > c1) continue;
+            const float w = ex2(ml[u].x - ms);
+            L = fmaf(ml[u].y, w, L);
+            acc.x = fmaf(o[u].x, w, acc.x);
+            acc.y = fmaf(o[u].y, w, acc.y);
+            acc.z = fmaf(o[u].z, w, acc.z);
+            acc.w = fmaf(o[u].w, w, acc.w);
+        }
+    }
+    const float inv = 1.f / L;
+    uint2 h = make_uint2(tc::pack_bf16(acc.x * inv, acc.y * inv), tc::pack_bf16(acc.z * inv, acc.w * inv));
+    if (absent) h = make_uint2(0, 0);
+    const size_t at = (size_t)bg * p.R + row;
+    *reinterpret_cast<uint2*>(p.out + at * D + 4 * col4) = h;
+    if (col4 == 0) p.lse[at] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int D>
@@ -550,6 +605,23 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
             }
             fence_before_sync();
+            if (p.count && !s.whole) {
+                // few rows: the unit's last CTA merges (one tile, so these are all 256
+                // threads), which spares a launch
+                __threadfence();
+                tc::named_sync(1 + X, 256);
+                unsigned* flag = reinterpret_cast<unsigned*>(smem + Cfg::OFF_MAX);
+                if (threadIdx.x == 64) {
+                    const unsigned before = atomicAdd(p.count + s.bg, 1u);
+                    *flag = before == (unsigned)p.split.k - 1;
+                    if (*flag) p.count[s.bg] = 0;
+                }
+                tc::named_sync(1 + X, 256);
+                if (*flag) {
+                    __threadfence();
+                    for (int e = threadIdx.x - 64; e < p.R * (D / 4); e += 256) merge_row<D>(p, s.bg, e % p.R, e / p.R);
+                }
+            }
         }
     }
     fence_before_sync();
@@ -560,53 +632,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     }
 }
 
-// Merges the parts of the units that were divided: with the parts' maxima m and
-// sums l, M = max m, L = sum l 2^(m - M), O = sum 2^(m - M) O_part / L, in the
-// order of the parts. One thread per four columns of a row; a block takes 1024 / D
-// consecutive rows, neighbouring lanes neighbouring rows, as the parts lie.
+// Merges the units that were divided, but those that their last CTA merged. One
+// thread per four columns of a row; a block takes 1024 / D consecutive rows,
+// neighbouring lanes neighbouring rows, as the parts lie.
 template <int D>
 __global__ void __launch_bounds__(256)
 tree_combine_kernel(const TreeParams p, unsigned rows) {
     griddep_wait();
     constexpr unsigned kRows = 1024 / D;
     const unsigned g = blockIdx.x * kRows + threadIdx.x % kRows;
-    const int col4 = threadIdx.x / kRows;
-    if (g >= rows) return;
-    const int row = (int)(g % (unsigned)p.R);
-    const int b0 = (int)(g / (unsigned)p.R * p.pairs + row / kUnitRows) * p.nb;
-    const int c0 = p.split.owner(b0), c1 = p.split.owner(b0 + p.nb - 1);
-    if (c0 == c1) return;  // written whole
-    // where CTA c left its part: the unit is the first one of every CTA but, it may be, c0
-    const bool second = p.split.first(c0) < b0;
-    auto part = [&](int c) { return (size_t)(2 * c + (c == c0 && second ? 1 : 0)); };
-    const int r = row % kUnitRows;
-    float M = -INFINITY;
-    bool absent = false;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float m = p.part_ml[part(c) * kUnitRows + r].x;
-        absent |= m != m;
-        M = fmaxf(M, m);
-    }
-    const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float2 ml = p.part_ml[part(c) * kUnitRows + r];
-        const float4 o = p.part_o[(part(c) * (D / 4) + col4) * kUnitRows + r];
-        const float w = ex2(ml.x - ms);
-        L = fmaf(ml.y, w, L);
-        acc.x = fmaf(o.x, w, acc.x);
-        acc.y = fmaf(o.y, w, acc.y);
-        acc.z = fmaf(o.z, w, acc.z);
-        acc.w = fmaf(o.w, w, acc.w);
-    }
-    const float inv = 1.f / L;
-    uint2 h = make_uint2(tc::pack_bf16(acc.x * inv, acc.y * inv), tc::pack_bf16(acc.z * inv, acc.w * inv));
-    if (absent) h = make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(p.out + (size_t)g * D + 4 * col4) = h;
-    if (col4 == 0) p.lse[g] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (g < rows) merge_row<D>(p, g / (unsigned)p.R, (int)(g % (unsigned)p.R), threadIdx.x / kRows);
 }
 
 template <int D>
@@ -652,11 +687,15 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.part_o = reinterpret_cast<float4*>(a.part);
     p.part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * a.num_sms * kUnitRows * D);
     p.wb = a.wb;
+    // Up to kMergeRows rows per KV head are merged by the unit's last CTA: measured,
+    // one token over 2048 slots, T1_FUSED us a pass against T1_KERNEL with a kernel.
+    constexpr int kMergeRows = 32;
+    p.count = by_unit && R <= kMergeRows ? a.count : nullptr;
     cudaError_t e = launch_ex(false, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
     bool divided = false;
     for (int c = 1; c < ctas && !divided; ++c) divided = p.split.first(c) % p.nb != 0;
-    if (!divided) return cudaSuccess;
+    if (!divided || p.count) return cudaSuccess;
     const unsigned rows = (unsigned)(groups * R);  // a [B,Hq,T,d] tensor of 2^32 rows does not fit the card
     return launch_ex(true, tree_combine_kernel<D>, dim3((rows + 1024 / D - 1) / (1024 / D)), dim3(256), 0, a.stream, p, rows);
 }
