@@ -43,6 +43,7 @@ using tc::fence_before_sync;
 
 constexpr int kThreads = 320;   // loader, MMA issuer, two warpgroups
 constexpr int kConsumers = 256;
+constexpr int kMaxCluster = 4;
 
 struct CkptTcParams {
     int B, Hq, Hkv, T, C, n;
@@ -448,12 +449,14 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const int groups = p.B * p.Hkv;
     // blocks in decreasing work: cache blocks (all rows see them), chunk blocks,
     // blocks of empty slots (zeros)
-    const int kb = blockIdx.x / groups, bg = blockIdx.x % groups;
+    const int rank = tc::cluster_rank(), ranks = tc::cluster_size();  // the cluster's CTAs share a key block
+    const int unit = blockIdx.x / ranks;
+    const int kb = unit / groups, bg = unit % groups;
     if (kb >= p.nbc + p.n_mblk) {
         const int s0 = 128 * (kb - p.n_mblk);
         const size_t at = ((size_t)bg * p.C + s0) * D;
         const int vecs = min(128, p.C - s0) * D / 8;
-        for (int e = threadIdx.x; e < vecs; e += kThreads) {
+        for (int e = rank * kThreads + threadIdx.x; e < vecs; e += ranks * kThreads) {
             reinterpret_cast<uint4*>(p.dK + at)[e] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4*>(p.dV + at)[e] = make_uint4(0, 0, 0, 0);
         }
@@ -463,7 +466,9 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const int t0 = cache ? 0 : 128 * (kb - p.nbc);  // first chunk token of the block
     const int m_first = t0 / 128;                   // query tiles before it see none of a chunk block
     const int per_head = p.n_mblk - m_first;
-    const int ntiles = G * per_head;
+    // query tiles of the KV head, heads one after the other; this CTA's are
+    // first .. first + ntiles - 1
+    const int first = G * per_head * rank / ranks, ntiles = G * per_head * (rank + 1) / ranks - first;
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -499,7 +504,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             for (; t < ntiles; ++t) {
                 const int s = t & 1;
                 if (!wait_bar(t_empty + s, ((t >> 1) & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag)) break;
-                const int bh = bg * G + t / per_head, m = m_first + t % per_head;
+                const int bh = bg * G + (first + t) / per_head, m = m_first + (first + t) % per_head;
                 uint8_t* dst = smem + Cfg::OFF_T + s * 2 * Cfg::TILE;
                 uint8_t* rows = smem + Cfg::OFF_ROW + s * 1024;
                 mbar_arrive_expect_tx(t_full + s, 2 * Cfg::TILE + 1024);
@@ -537,7 +542,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                                      Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
         };
         constexpr uint64_t kStage = (2 * Cfg::TILE) >> 4, kDO = Cfg::TILE >> 4;
-        bool ok = warp_wait(kv_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag) &&
+        bool ok = ntiles > 0 && warp_wait(kv_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag) &&
                   warp_wait(t_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag);
         if (ok) {
             issue_ss(tmem, dK, dTk);
@@ -602,7 +607,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 x[3] = __float_as_uint(ex2(b.y));
             }
             // the diagonal tile: row c sees key kr if c >= kr
-            if (!cache && t % per_head == 0) {
+            if (!cache && (first + t) % per_head == 0) {
                 const int lo = kr - 64 * wg;
 #pragma unroll
                 for (int e = 0; e < 64; ++e)
@@ -643,25 +648,71 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         }
         if (ok && warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag)) {
             fence_after_sync();
-            // the first warpgroup writes dV, the second dK; slots n.. of the last cache block get zeros
-            const int key = (cache ? 128 * kb : t0) + kr;
-            const bool in = key < (cache ? p.C : p.T), valid = !cache || key < p.n;
-            __nv_bfloat16* base = wg ? (cache ? p.dK : p.dk) : (cache ? p.dV : p.dv);
-            __nv_bfloat16* dst = base + ((size_t)bg * (cache ? p.C : p.T) + key) * D;
+            // into shared memory, where the query tiles were: dV by the first warpgroup,
+            // dK by the second; 16-byte chunks of a row are permuted by the row, so that
+            // neither these stores nor the loads below meet in a bank
+            float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_T) + (wg * 128 + kr) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(tmem + lane_off + 256 + wg * D + c, o);
+                tc::tmem_ld_wait();
+                tc::reg_fence(o);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) store_acc64(tmem + lane_off + 256 + wg * D + 64 * c, dst + 64 * c, wg ? p.scale : 1.f, in && valid);
-            if (in && !valid) {
-#pragma unroll
-                for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4*>(acc + (((c + e) / 4) ^ (kr & (D / 4 - 1))) * 4) =
+                        ntiles ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0, 0, 0, 0);
             }
         }
     }
     fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    tc::cluster_sync();
     if (warp == 1) {
         fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
+    // each CTA adds up its share of the keys over the cluster, in the order of its
+    // CTAs; slots n.. of the last cache block get zeros
+    const int key0 = cache ? 128 * kb : t0, keys = min(128, (cache ? p.C : p.T) - key0);
+    const int k0 = 128 * rank / ranks, k1 = min(keys, 128 * (rank + 1) / ranks);
+    for (int e = threadIdx.x; e < 2 * (k1 - k0) * (D / 4); e += kThreads) {
+        const int c4 = e % (D / 4), k = k0 + e / (D / 4) % (k1 - k0), part = e / (D / 4) / (k1 - k0);
+        const uint32_t at = sbase + Cfg::OFF_T + ((part * 128 + k) * D + (c4 ^ (k & (D / 4 - 1))) * 4) * 4;
+        float4 a = tc::cluster_load4(at, 0);
+        for (int q = 1; q < ranks; ++q) {
+            const float4 x = tc::cluster_load4(at, q);
+            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+        }
+        const float mul = part ? p.scale : 1.f;
+        uint2 h = make_uint2(tc::pack_bf16(a.x * mul, a.y * mul), tc::pack_bf16(a.z * mul, a.w * mul));
+        if (cache && key0 + k >= p.n) h = make_uint2(0, 0);
+        __nv_bfloat16* base = part ? (cache ? p.dK : p.dk) : (cache ? p.dV : p.dv);
+        *reinterpret_cast<uint2*>(base + ((size_t)bg * (cache ? p.C : p.T) + key0 + k) * D + 4 * c4) = h;
+    }
+    tc::cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// CTAs per key block of the dK / dV kernel. A block's query tiles are divided among
+// a cluster when there are few blocks, or when whole blocks leave SMs idle at the
+// end. The estimate, in tiles: what an SM has to do, half of a CTA's tiles as the
+// unevenness of the last round, and kCtaTiles for what every CTA does besides.
+int cluster_for(int groups, int G, int n_mblk, int nbc, int num_sms) {
+    constexpr double kCtaTiles = 2.0;
+    const double units = (double)groups * (nbc + n_mblk);
+    const double sum = (double)groups * G * n_mblk * (nbc + 0.5 * (n_mblk + 1));
+    const double most = G * n_mblk;
+    double best = 0;
+    int s_best = 1;
+    for (int s = 1; s <= kMaxCluster && s <= most; ++s) {
+        const double ctas = units * s;
+        const double t = ctas <= num_sms ? most / s + kCtaTiles : sum / num_sms + 0.5 * most / s + kCtaTiles * ctas / num_sms;
+        if (s == 1 || t < best) {
+            best = t;
+            s_best = s;
+        }
+    }
+    return s_best;
 }
 
 template <int D>
@@ -698,8 +749,19 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     cudaError_t e = launch_ex(false, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.n_mblk * heads)), dim3(kThreads),
                               DqCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
-    return launch_ex(false, ckpt_dkdv_tc_kernel<D>, dim3((unsigned)((p.nbC + p.n_mblk) * groups)), dim3(kThreads),
-                     DkvCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
+    const int ranks = cluster_for((int)groups, a.Hq / a.Hkv, p.n_mblk, p.nbc, a.num_sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.nbC + p.n_mblk) * groups * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = DkvCfg<D>::SMEM;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ckpt_dkdv_tc_kernel<D>, mq, mdo, mkc, mvc, mk, mv, p);
 }
 
 }  // namespace
