@@ -204,6 +204,16 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
         if (!aligned16(p)) return fail(c, H2O_ERR_ALIGN, "every pointer argument must be 16-byte aligned");
     DeviceGuard g(c->device);
     cudaStream_t s = (cudaStream_t)stream;
+    CkptBwdArgs a{};
+    a.B = c->B;
+    a.Hq = c->Hq;
+    a.Hkv = c->Hkv;
+    a.d = c->d;
+    a.C = c->C;
+    a.T = T;
+    a.n = n;
+    a.dtype = c->dtype;
+    a.num_sms = c->num_sms;
     // workspace: the restored step and the statistics of its rows
     const int pitch = std::max(n, 1);
     const size_t groups = (size_t)c->B * c->Hkv;
@@ -215,7 +225,7 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
         return at;
     };
     const size_t oq = take(nq * c->elem), ok = take(nk * c->elem), ov = take(nk * c->elem);
-    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(c->B, c->Hq, T));
+    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(a));
     rc = checkpoint_workspace(c, end, s);
     if (rc != H2O_OK) return rc;
     char* w = static_cast<char*>(c->ckpt_ws);
@@ -229,15 +239,6 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     r.pitch = pitch;
     H2O_TRY(c, launch_ckpt_restore(r), "launch checkpoint restore");
 
-    CkptBwdArgs a{};
-    a.B = c->B;
-    a.Hq = c->Hq;
-    a.Hkv = c->Hkv;
-    a.d = c->d;
-    a.C = c->C;
-    a.T = T;
-    a.n = n;
-    a.dtype = c->dtype;
     a.q = r.q;
     a.k = r.k;
     a.v = r.v;
@@ -254,7 +255,6 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     a.wb.err_word = c->err_dev;
     a.wb.ns = c->wait_ns;
     a.stream = s;
-    a.num_sms = c->num_sms;
     H2O_TRY(c, c->use_tc ? launch_ckpt_backward_tc(a) : launch_ckpt_backward_simt(a), "launch checkpoint backward");
     return H2O_OK;
 }

@@ -2,16 +2,22 @@
 // backward of a step's attention at the values an 8-bit checkpoint stands for
 // (bf16; the formulas are ckpt_backward.cu's).
 //
-// ckpt_dq_tc_kernel    one CTA per (128-row query tile, head), two passes over
-//     the tile's key blocks. The first computes S = Q K^T and dP = dO V^T and
-//     keeps each row's running maximum m, sum l = sum e and w = sum e dp
-//     (e = 2^(s - m)); then LSE = m + log2 l and D = w / l, in fp32. The second
-//     recomputes both products, writes dS = P (dP - D) as bf16 over S in TMEM
-//     and accumulates dQ += dS K with dS as the A operand from TMEM.
-// ckpt_dkdv_tc_kernel  one CTA per (KV head, 128-key block), one key per TMEM
-//     lane: per 128-row query tile of the KV head, S^T = K Q^T and
-//     dP^T = V dO^T; P^T and dS^T go back over them as bf16 and are the A
-//     operands of dV += P^T dO and dK += dS^T Q.
+// The query rows of a KV head, R = G T of them (row = head-in-group * T + token),
+// are cut into 128-row tiles whatever their heads, so that short chunks fill them;
+// the keys into 128-key blocks, the cache's and the chunk's.
+//
+// ckpt_dq_tc_kernel    one CTA per query tile, two passes over the tile's key blocks.
+//     The first computes S = Q K^T and dP = dO V^T and keeps each row's running
+//     maximum m, sum l = sum e and w = sum e dp (e = 2^(s - m)); then
+//     LSE = m + log2 l and D = w / l, in fp32. The second recomputes both products,
+//     writes dS = P (dP - D) as bf16 over S in TMEM and accumulates dQ += dS K with
+//     dS as the A operand from TMEM. Where tiles are few, their blocks are divided
+//     among several CTAs: one launch for the first pass, one for the second, and
+//     ckpt_dq_combine_kernel adds up the parts in order.
+// ckpt_dkdv_tc_kernel  one CTA, or a cluster, per (KV head, 128-key block), one key
+//     per TMEM lane: per query tile of the KV head, S^T = K Q^T and dP^T = V dO^T;
+//     P^T and dS^T go back over them as bf16 and are the A operands of
+//     dV += P^T dO and dK += dS^T Q.
 //
 // Bound by the tensor core: 5 products of 2 d per visible (row, key) in the
 // first kernel, 4 in the second. An operand pair from shared memory needs
@@ -22,11 +28,13 @@
 // does not wait for the exponentials in progress: dV(t), S(t+1) while dS(t) is
 // computed, dK(t), dP(t+1) while P(t+1) is.
 //
-// Rows past the end of a head or cache arrive as zeros (3-D tensor maps), so
+// Rows past the end of a KV head or cache arrive as zeros (3-D tensor maps), so
 // nothing of another head enters a tile. P and dS are rounded to bf16, the MMA's
 // operand type; statistics and gradients accumulate in fp32.
 #include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "operators.h"
 #include "tc.h"
@@ -47,12 +55,18 @@ constexpr int kMaxCluster = 4;
 
 struct CkptTcParams {
     int B, Hq, Hkv, T, C, n;
-    int n_mblk;  // 128-row query tiles per head
+    int R;       // query rows per KV head
+    int tiles;   // 128-row query tiles per KV head
+    int n_mblk;  // chunk key blocks = ceil(T / 128)
     int nbc;     // cache key blocks = ceil(n / 128)
     int nbC;     // 128-slot blocks of the whole cache
+    int passes;  // dQ kernel: bit 0 the first pass, bit 1 the second
+    int parts;   // dQ kernel: CTAs per query tile
     float scale_log2, scale;
-    float* nL2;  // [B*Hq][128 * n_mblk]: -(log2-domain LSE) per row, -inf in padding rows
-    float* D;    // [B*Hq][128 * n_mblk], 0 in padding rows
+    float* nL2;     // [B*Hkv][128 * tiles]: -(log2-domain LSE) per row, -inf in padding rows
+    float* D;       // [B*Hkv][128 * tiles], 0 in padding rows
+    float4* stat;   // parts > 1: [parts][B*Hkv][128 * tiles]: m, l, w of a part
+    float4* part;   // parts > 1: [parts][B*Hkv * tiles][D / 4][128]: four columns of dQ
     __nv_bfloat16* dq;
     __nv_bfloat16* dK;
     __nv_bfloat16* dV;
@@ -61,24 +75,10 @@ struct CkptTcParams {
     WaitBound wb;
 };
 
-// 64 accumulator columns of this thread's lane, times mul, as 128 bytes of bf16.
-__device__ __forceinline__ void store_acc64(uint32_t taddr, __nv_bfloat16* dst, float mul, bool in) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        tc::tmem_ld32(taddr + 32 * c, o);
-        tc::tmem_ld_wait();
-        tc::reg_fence(o);
-        if (in) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(dst + 32 * c + e) =
-                    make_uint4(tc::pack_bf16(__uint_as_float(o[e]) * mul, __uint_as_float(o[e + 1]) * mul),
-                               tc::pack_bf16(__uint_as_float(o[e + 2]) * mul, __uint_as_float(o[e + 3]) * mul),
-                               tc::pack_bf16(__uint_as_float(o[e + 4]) * mul, __uint_as_float(o[e + 5]) * mul),
-                               tc::pack_bf16(__uint_as_float(o[e + 6]) * mul, __uint_as_float(o[e + 7]) * mul));
-        }
-    }
+// Chunk key blocks that some row of a query tile sees (at least one).
+__device__ __forceinline__ int chunk_blocks(const CkptTcParams& p, int tile) {
+    const int r0 = 128 * tile, r1 = min(p.R, r0 + 128) - 1;
+    return (r1 / p.T > r0 / p.T ? p.T - 1 : r1 % p.T) / 128 + 1;
 }
 
 // ============================================================================
@@ -126,12 +126,15 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int per_mblk = p.B * p.Hq;
-    const int mblk = p.n_mblk - 1 - (int)(blockIdx.x / per_mblk);  // most key blocks first
-    const int bh = blockIdx.x % per_mblk;
-    const int bg = bh / (p.Hq / p.Hkv);
-    const int m0 = mblk * 128;
-    const int nb = p.nbc + mblk + 1;  // key blocks per pass: cache, then chunk 0..mblk
+    const int part = blockIdx.x % p.parts, unit = blockIdx.x / p.parts;
+    const int groups = p.B * p.Hkv, bg = unit % groups;
+    int tile = p.tiles - 1 - unit / groups;
+    if (p.T % 128 == 0)  // the heads' last tiles first: they have the most key blocks
+        tile = unit / groups % (p.tiles / p.n_mblk) * p.n_mblk + p.n_mblk - 1 - unit / groups / (p.tiles / p.n_mblk);
+    const int m0 = tile * 128;
+    const int all = p.nbc + chunk_blocks(p, tile);  // key blocks: cache, then chunk
+    const int jb = all * part / p.parts, nb = all * (part + 1) / p.parts - jb;  // this CTA's
+    const bool pass1 = p.passes & 1, pass2 = p.passes & 2;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -162,13 +165,14 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         if (lane == 0) {
             mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE);
             for (int hh = 0; hh < D / 64; ++hh) {
-                tc::tma_load_3d(smem + Cfg::OFF_Q + hh * Cfg::HALF, &map_q, 64 * hh, m0, bh, q_full);
-                tc::tma_load_3d(smem + Cfg::OFF_DO + hh * Cfg::HALF, &map_do, 64 * hh, m0, bh, q_full);
+                tc::tma_load_3d(smem + Cfg::OFF_Q + hh * Cfg::HALF, &map_q, 64 * hh, m0, bg, q_full);
+                tc::tma_load_3d(smem + Cfg::OFF_DO + hh * Cfg::HALF, &map_do, 64 * hh, m0, bg, q_full);
             }
             int L = 0;
             bool ok = true;
-            for (int it = 0; ok && it < 2 * nb; ++it) {
-                const int j = it % nb;
+            const int rounds = (pass1 ? nb : 0) + (pass2 ? nb : 0);
+            for (int it = 0; ok && it < rounds; ++it) {
+                const int j = jb + it % nb;
                 const bool cache = j < p.nbc;
                 const int row = 128 * (cache ? j : j - p.nbc);
                 for (int kv = 0; kv < 2; ++kv, ++L) {
@@ -209,7 +213,8 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         };
         bool ok = warp_wait(q_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag);
         // pass 1: S and dP of block t into buffer t & 1
-        for (int t = 0; ok && t < nb; ++t) {
+        const int n1 = pass1 ? nb : 0, n2 = pass2 ? nb : 0;
+        for (int t = 0; ok && t < n1; ++t) {
             const int b = t & 1, ks = 2 * t, vs = 2 * t + 1;
             ok = (t < 2 || warp_wait(sd_free + b, ((t >> 1) - 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag)) && wait_ring(ks);
             if (!ok) break;
@@ -222,10 +227,10 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             tc::mma_commit_warp(ring_empty + vs % RING);
         }
         // pass 2: S(t) and then dS(t) in buffer t & 1, one dP, dQ
-        for (int b = 0; b < 2 && b < nb; ++b)  // both buffers read
-            ok = ok && warp_wait(sd_free + b, ((nb - 1 - b) >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+        for (int b = 0; b < 2 && b < n1; ++b)  // both buffers read
+            ok = ok && warp_wait(sd_free + b, ((n1 - 1 - b) >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
         fence_after_sync();
-        const int L0 = 2 * nb;
+        const int L0 = 2 * n1;
         auto issue_s = [&](int t) {  // needs buffer t & 1 free, or read by products issued before
             const int l = L0 + 2 * t;
             if (!wait_ring(l)) return false;
@@ -241,11 +246,11 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             tc::mma_commit_warp(ring_empty + l % RING);
             return true;
         };
-        ok = ok && issue_s(0) && issue_dp(0) && (nb < 2 || issue_s(1));
-        for (int t = 0; ok && t < nb; ++t) {
+        ok = ok && (n2 < 1 || (issue_s(0) && issue_dp(0))) && (n2 < 2 || issue_s(1));
+        for (int t = 0; ok && t < n2; ++t) {
             if (!(ok = warp_wait(ds_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
-            if (t + 1 < nb && !(ok = issue_dp(t + 1))) break;
+            if (t + 1 < n2 && !(ok = issue_dp(t + 1))) break;
             const int ks = (L0 + 2 * t) % RING;
             const uint64_t b = dRingN + (uint64_t)((ks * Cfg::TILE) >> 4);
 #pragma unroll
@@ -253,7 +258,7 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
                 tc::mma_bf16_ts_warp(tmem + 384, tmem + 128 * (t & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
                                      b + (uint64_t)((kk * 16 * 128) >> 4), Cfg::IDESC_G, (t > 0 || kk > 0) ? 1u : 0u);
             tc::mma_commit_warp(ring_empty + ks);
-            if (t + 2 < nb) ok = issue_s(t + 2);
+            if (t + 2 < n2) ok = issue_s(t + 2);
         }
         // all MMAs issued here complete before TMEM can be released
         tc::mma_commit_warp(drain);
@@ -266,11 +271,15 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         const int r = quad * 32 + lane;  // row inside the tile = TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + 64 * wg;
         float* st = reinterpret_cast<float*>(smem + Cfg::OFF_ST);
-        // visible columns of this row's half in block j: e < limit
-        auto limit_of = [&](int j) { return (j < p.nbc ? p.n - 128 * j : m0 + r - 128 * (j - p.nbc) + 1) - 64 * wg; };
+        const int token = (m0 + r) % p.T;
+        // visible columns of this row's half in this CTA's block t: e < limit
+        auto limit_of = [&](int t) {
+            const int j = jb + t;
+            return (j < p.nbc ? p.n - 128 * j : token - 128 * (j - p.nbc) + 1) - 64 * wg;
+        };
         float m = -INFINITY, l = 0.f, w = 0.f;
         bool ok = true;
-        for (int t = 0; t < nb; ++t) {
+        for (int t = 0; pass1 && t < nb; ++t) {
             const int b = t & 1;
             if (!(ok = warp_wait(sd_full + b, (t >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
@@ -319,7 +328,8 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         }
         // the two halves of a row meet: the second hands over its m, l and w, the
         // first gives back -LSE and D
-        const bool row_ok = m0 + r < p.T;
+        const bool row_ok = m0 + r < p.R;
+        const size_t at = ((size_t)bg * p.tiles + tile) * 128 + r, all_rows = (size_t)groups * p.tiles * 128;
         float nL2, Dr;
         if (wg == 1) {
             st[r] = m;
@@ -331,20 +341,39 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             Dr = st[128 + r];
         } else {
             tc::named_sync(1, kConsumers);
-            const float M = fmaxf(m, st[r]);
-            const float a0 = ex2(m - M), a1 = ex2(st[r] - M);
-            const float L = l * a0 + st[128 + r] * a1;
+            float M = fmaxf(m, st[r]);
+            float Ms = M == -INFINITY ? 0.f : M;
+            const float a0 = ex2(m - Ms), a1 = ex2(st[r] - Ms);
+            float L = l * a0 + st[128 + r] * a1, W = w * a0 + st[256 + r] * a1;
+            if (p.parts > 1) {
+                if (pass1) {
+                    p.stat[part * all_rows + at] = make_float4(M, L, W, 0.f);
+                } else {
+                    // the parts of a tile, in order
+                    M = -INFINITY;
+                    for (int q = 0; q < p.parts; ++q) M = fmaxf(M, p.stat[q * all_rows + at].x);
+                    Ms = M == -INFINITY ? 0.f : M;
+                    L = W = 0.f;
+                    for (int q = 0; q < p.parts; ++q) {
+                        const float4 x = p.stat[q * all_rows + at];
+                        const float a = ex2(x.x - Ms);
+                        L = fmaf(x.y, a, L);
+                        W = fmaf(x.z, a, W);
+                    }
+                }
+            }
             nL2 = -(M + log2f(L));
-            Dr = (w * a0 + st[256 + r] * a1) / L;
+            Dr = W / L;
             st[r] = nL2;
             st[128 + r] = Dr;
             tc::named_sync(2, kConsumers);
-            const size_t at = ((size_t)bh * p.n_mblk + mblk) * 128 + r;
-            p.nL2[at] = row_ok ? nL2 : -INFINITY;
-            p.D[at] = row_ok ? Dr : 0.f;
+            if (pass2 && part == 0) {
+                p.nL2[at] = row_ok ? nL2 : -INFINITY;
+                p.D[at] = row_ok ? Dr : 0.f;
+            }
         }
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nL2, nL2), nd2 = make_float2(-Dr, -Dr);
-        for (int t = 0; ok && t < nb; ++t) {
+        for (int t = 0; pass2 && ok && t < nb; ++t) {
             const uint32_t tS = tl + 128 * (t & 1);
             if (!(ok = warp_wait(s_full + (t & 1), (t >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
@@ -355,17 +384,17 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
 #pragma unroll
             for (int c = 0; c < 2; ++c) tc::reg_fence(s[c]);
             const int limit = limit_of(t);
+            if (limit < 64) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e >= limit) s[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+            }
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
                 const float2 x = tc::ffma2(
                     make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), sc2, nl2);
                 s[e >> 5][e & 31] = __float_as_uint(ex2(x.x));
                 s[e >> 5][(e & 31) + 1] = __float_as_uint(ex2(x.y));
-            }
-            if (limit < 64) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e >= limit) s[e >> 5][e & 31] = 0u;
             }
             if (!(ok = warp_wait(dp_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
@@ -388,10 +417,43 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
         }
-        if (ok && warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag)) {
-            fence_after_sync();
-            if (64 * wg < D)
-                store_acc64(tl + 384, p.dq + ((size_t)bh * p.T + m0 + r) * D + 64 * wg, p.scale, row_ok);
+        if (ok) ok = warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
+        fence_after_sync();
+        // dQ: this thread has D / 2 columns of its row. A part goes to memory as it is,
+        // rows next to each other; the whole goes through shared memory (the key ring is
+        // done with), 16-byte chunks permuted by the row so that no bank is met twice
+        constexpr int kCols = D / 2;
+        const int col0 = kCols * wg;
+        const uint32_t tQ = tmem + ((uint32_t)(quad * 32) << 16) + 384 + col0;
+        float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_RING);
+        if (pass2 && ok) {
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(tQ + c, o);
+                tc::tmem_ld_wait();
+                tc::reg_fence(o);
+                float4* dst = p.part + ((((size_t)part * groups + bg) * p.tiles + tile) * (D / 4) + (col0 + c) / 4) * 128 + r;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                                 __uint_as_float(o[e + 3]));
+                    if (p.parts > 1)
+                        dst[e / 4 * 128] = x;
+                    else
+                        *reinterpret_cast<float4*>(acc + r * D + (((col0 + c + e) / 4) ^ (r & (D / 4 - 1))) * 4) = x;
+                }
+            }
+        }
+        if (pass2 && p.parts == 1) {
+            tc::named_sync(1, kConsumers);
+            const int rows = min(128, p.R - m0);
+            for (int e = threadIdx.x - 64; e < rows * (D / 4); e += kConsumers) {
+                const int rr = e / (D / 4), c4 = e % (D / 4);
+                const float4 x = *reinterpret_cast<const float4*>(acc + rr * D + (c4 ^ (rr & (D / 4 - 1))) * 4);
+                *reinterpret_cast<uint2*>(p.dq + ((size_t)bg * p.R + m0 + rr) * D + 4 * c4) =
+                    make_uint2(tc::pack_bf16(x.x * p.scale, x.y * p.scale), tc::pack_bf16(x.z * p.scale, x.w * p.scale));
+            }
         }
     }
     fence_before_sync();
@@ -399,6 +461,25 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     if (warp == 1) {
         fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// dQ of a row from the parts of its tile, in order; one thread per four columns,
+// neighbouring lanes neighbouring rows, as the parts lie.
+template <int D>
+__global__ void __launch_bounds__(256) ckpt_dq_combine_kernel(const CkptTcParams p) {
+    const int r = threadIdx.x % 32 + 32 * (blockIdx.x % 4), unit = blockIdx.x / 4;  // KV head and tile
+    const int row = unit % p.tiles * 128 + r;
+    if (row >= p.R) return;
+    for (int c4 = threadIdx.x / 32; c4 < D / 4; c4 += 8) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int q = 0; q < p.parts; ++q) {
+            const float4 x = p.part[(((size_t)q * p.B * p.Hkv * p.tiles + unit) * (D / 4) + c4) * 128 + r];
+            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+        }
+        *reinterpret_cast<uint2*>(p.dq + ((size_t)(unit / p.tiles) * p.R + row) * D + 4 * c4) =
+            make_uint2(tc::pack_bf16(a.x * p.scale, a.y * p.scale), tc::pack_bf16(a.z * p.scale, a.w * p.scale));
     }
 }
 
@@ -445,7 +526,6 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int G = p.Hq / p.Hkv;
     const int groups = p.B * p.Hkv;
     // blocks in decreasing work: cache blocks (all rows see them), chunk blocks,
     // blocks of empty slots (zeros)
@@ -464,11 +544,15 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     }
     const bool cache = kb < p.nbc;
     const int t0 = cache ? 0 : 128 * (kb - p.nbc);  // first chunk token of the block
-    const int m_first = t0 / 128;                   // query tiles before it see none of a chunk block
-    const int per_head = p.n_mblk - m_first;
-    // query tiles of the KV head, heads one after the other; this CTA's are
-    // first .. first + ntiles - 1
-    const int first = G * per_head * rank / ranks, ntiles = G * per_head * (rank + 1) / ranks - first;
+    // this CTA's query tiles: of those of the KV head that see a key of the block,
+    // every ranks-th one; next() gives the one after `tile` (p.tiles: none)
+    auto next = [&](int tile, int steps) {
+        if (t0 == 0) return min(tile + steps, p.tiles);
+        while (steps > 0 && ++tile < p.tiles) steps -= 128 * (chunk_blocks(p, tile) - 1) >= t0;
+        return tile;
+    };
+    const int first = next(-1, rank + 1);
+    const bool any = first < p.tiles;
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -501,18 +585,17 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 tc::tma_load_3d(smem + Cfg::OFF_V + hh * Cfg::HALF, cache ? &map_vc : &map_v, 64 * hh, krow, bg, kv_full);
             }
             int t = 0;
-            for (; t < ntiles; ++t) {
+            for (int tile = first; tile < p.tiles; tile = next(tile, ranks), ++t) {
                 const int s = t & 1;
                 if (!wait_bar(t_empty + s, ((t >> 1) & 1) ^ 1, p.wb, kDevTimeoutSlotWait, abort_flag)) break;
-                const int bh = bg * G + (first + t) / per_head, m = m_first + (first + t) % per_head;
                 uint8_t* dst = smem + Cfg::OFF_T + s * 2 * Cfg::TILE;
                 uint8_t* rows = smem + Cfg::OFF_ROW + s * 1024;
                 mbar_arrive_expect_tx(t_full + s, 2 * Cfg::TILE + 1024);
                 for (int x = 0; x < D / 64; ++x) {
-                    tc::tma_load_3d(dst + x * Cfg::HALF, &map_q, 64 * x, 128 * m, bh, t_full + s);
-                    tc::tma_load_3d(dst + Cfg::TILE + x * Cfg::HALF, &map_do, 64 * x, 128 * m, bh, t_full + s);
+                    tc::tma_load_3d(dst + x * Cfg::HALF, &map_q, 64 * x, 128 * tile, bg, t_full + s);
+                    tc::tma_load_3d(dst + Cfg::TILE + x * Cfg::HALF, &map_do, 64 * x, 128 * tile, bg, t_full + s);
                 }
-                const size_t at = ((size_t)bh * p.n_mblk + m) * 128;
+                const size_t at = ((size_t)bg * p.tiles + tile) * 128;
                 tc::bulk_load(rows, p.nL2 + at, 512, t_full + s);
                 tc::bulk_load(rows + 512, p.D + at, 512, t_full + s);
             }
@@ -542,7 +625,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                                      Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
         };
         constexpr uint64_t kStage = (2 * Cfg::TILE) >> 4, kDO = Cfg::TILE >> 4;
-        bool ok = ntiles > 0 && warp_wait(kv_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag) &&
+        bool ok = any && warp_wait(kv_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag) &&
                   warp_wait(t_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag);
         if (ok) {
             issue_ss(tmem, dK, dTk);
@@ -550,22 +633,25 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             issue_ss(tmem + 128, dV, dTk + kDO);
             tc::mma_commit_warp(dp_full);
         }
-        for (int t = 0; ok && t < ntiles; ++t) {
-            const uint64_t at = (t & 1) * kStage, next = kStage - at;
+        int t = 0;
+        for (int tile = first, after; ok && tile < p.tiles; tile = after, ++t) {
+            after = next(tile, ranks);
+            const bool more = after < p.tiles;
+            const uint64_t at = (t & 1) * kStage, ahead = kStage - at;
             if (!(ok = warp_wait(p_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
             issue_ts(tmem + 256, tmem, dTn + at + kDO, t == 0);  // dV += P^T dO
-            if (t + 1 < ntiles) {
+            if (more) {
                 if (!(ok = warp_wait(t_full + ((t + 1) & 1), ((t + 1) >> 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag))) break;
-                issue_ss(tmem, dK, dTk + next);
+                issue_ss(tmem, dK, dTk + ahead);
                 tc::mma_commit_warp(s_full);
             }
             if (!(ok = warp_wait(ds_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
             issue_ts(tmem + 256 + D, tmem + 128, dTn + at, t == 0);  // dK += dS^T Q
             tc::mma_commit_warp(t_empty + (t & 1));
-            if (t + 1 < ntiles) {
-                issue_ss(tmem + 128, dV, dTk + next + kDO);
+            if (more) {
+                issue_ss(tmem + 128, dV, dTk + ahead + kDO);
                 tc::mma_commit_warp(dp_full);
             }
         }
@@ -581,7 +667,8 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         const uint32_t tl = tmem + lane_off + 64 * wg;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        for (int t = 0; t < ntiles; ++t) {
+        int t = 0;
+        for (int tile = first; tile < p.tiles; tile = next(tile, ranks), ++t) {
             // the rows' statistics came with the tile
             const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROW + (t & 1) * 1024) + 64 * wg;
             if (!(ok = warp_wait(t_full + (t & 1), (t >> 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag) &&
@@ -594,6 +681,25 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             tc::tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 2; ++c) tc::reg_fence(s[c]);
+            // a chunk key is seen by the tokens from its own on: unless every row of the
+            // tile is one, each is compared (a tile may hold the end of one head and the
+            // start of another, or several heads)
+            if (!cache) {
+                const int i0 = 128 * tile % p.T;
+                if (i0 + 127 >= p.T || i0 < t0 + 127) {
+                    uint32_t vis[2] = {0u, 0u};
+                    for (int c = -((i0 + 64 * wg) % p.T); c < 64; c += p.T) {  // a head starts at column c
+                        const int lo = max(c + t0 + kr, 0), hi = min(c + p.T, 64);
+                        if (lo >= hi) continue;
+                        const unsigned long long ones = (~0ull >> (64 - (hi - lo))) << lo;
+                        vis[0] |= (uint32_t)ones;
+                        vis[1] |= (uint32_t)(ones >> 32);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (!((vis[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+                }
+            }
             uint32_t pk[32];
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
@@ -601,21 +707,14 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 uint32_t* x = &s[e >> 5][e & 31];
                 const float2 a = tc::ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, make_float2(nl.x, nl.y));
                 const float2 b = tc::ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, make_float2(nl.z, nl.w));
-                x[0] = __float_as_uint(ex2(a.x));
-                x[1] = __float_as_uint(ex2(a.y));
-                x[2] = __float_as_uint(ex2(b.x));
-                x[3] = __float_as_uint(ex2(b.y));
+                const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
+                x[0] = __float_as_uint(pa.x);
+                x[1] = __float_as_uint(pa.y);
+                x[2] = __float_as_uint(pb.x);
+                x[3] = __float_as_uint(pb.y);
+                pk[e >> 1] = tc::pack_bf16(pa.x, pa.y);
+                pk[(e >> 1) + 1] = tc::pack_bf16(pb.x, pb.y);
             }
-            // the diagonal tile: row c sees key kr if c >= kr
-            if (!cache && (first + t) % per_head == 0) {
-                const int lo = kr - 64 * wg;
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e < lo) s[e >> 5][e & 31] = 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 64; e += 2)
-                pk[e >> 1] = tc::pack_bf16(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
             tc::tmem_st32(tl, pk);
             tc::tmem_st_wait();
             fence_before_sync();
@@ -661,7 +760,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<uint4*>(acc + (((c + e) / 4) ^ (kr & (D / 4 - 1))) * 4) =
-                        ntiles ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0, 0, 0, 0);
+                        any ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -697,16 +796,18 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 // a cluster when there are few blocks, or when whole blocks leave SMs idle at the
 // end. The estimate, in tiles: what an SM has to do, half of a CTA's tiles as the
 // unevenness of the last round, and kCtaTiles for what every CTA does besides.
-int cluster_for(int groups, int G, int n_mblk, int nbc, int num_sms) {
-    constexpr double kCtaTiles = 2.0;
+// Measured, clusters of 1, 2, 3 and 4: 110.9, 104.7, 121.7, 128.8 us at T=1024
+// C=2048 d=128 (192 blocks of up to 32 tiles), 48.3, 28.6, 22.1, 30.1 us at B=2 T=333
+// C=1000 d=64 (40 blocks of up to 24).
+int cluster_for(int groups, int tiles, int n_mblk, int nbc, int num_sms) {
+    constexpr double kCtaTiles = 5.0;
     const double units = (double)groups * (nbc + n_mblk);
-    const double sum = (double)groups * G * n_mblk * (nbc + 0.5 * (n_mblk + 1));
-    const double most = G * n_mblk;
+    const double sum = (double)groups * tiles * (nbc + 0.5 * (n_mblk + 1));
     double best = 0;
     int s_best = 1;
-    for (int s = 1; s <= kMaxCluster && s <= most; ++s) {
-        const double ctas = units * s;
-        const double t = ctas <= num_sms ? most / s + kCtaTiles : sum / num_sms + 0.5 * most / s + kCtaTiles * ctas / num_sms;
+    for (int s = 1; s <= kMaxCluster && s <= tiles; ++s) {
+        const double ctas = units * s, most = (tiles + s - 1) / s;
+        const double t = ctas <= num_sms ? most + kCtaTiles : sum / num_sms + 0.5 * most + kCtaTiles * ctas / num_sms;
         if (s == 1 || t < best) {
             best = t;
             s_best = s;
@@ -715,14 +816,25 @@ int cluster_for(int groups, int G, int n_mblk, int nbc, int num_sms) {
     return s_best;
 }
 
+int dq_tiles(int Hq, int Hkv, int T) { return (Hq / Hkv * T + 127) / 128; }
+
+// CTAs per query tile of the dQ kernel: more than one only when the tiles fill less
+// than half of the SMs and have blocks enough to repay two more launches.
+int dq_parts(int groups, int tiles, int blocks, int num_sms) {
+    const int units = groups * tiles;
+    if (2 * units > num_sms || blocks < 8) return 1;
+    return std::min(num_sms / units, blocks / 2);
+}
+
 template <int D>
 cudaError_t backward_launch(const CkptBwdArgs& a) {
     if (cudaError_t e = ensure_smem_limit(ckpt_dq_tc_kernel<D>, DqCfg<D>::SMEM); e != cudaSuccess) return e;
     if (cudaError_t e = ensure_smem_limit(ckpt_dkdv_tc_kernel<D>, DkvCfg<D>::SMEM); e != cudaSuccess) return e;
     CUtensorMap mq, mdo, mkc, mvc, mk, mv;
-    const uint64_t heads = (uint64_t)a.B * a.Hq, groups = (uint64_t)a.B * a.Hkv;
+    const uint64_t groups = (uint64_t)a.B * a.Hkv;
+    const int R = a.Hq / a.Hkv * a.T;
     const uint64_t rows = a.n > 0 ? a.n : 1;  // an empty cache is never loaded from
-    if (!tc_make_map3(&mq, a.q, a.T, heads, a.T, D, 128) || !tc_make_map3(&mdo, a.dout, a.T, heads, a.T, D, 128) ||
+    if (!tc_make_map3(&mq, a.q, R, groups, R, D, 128) || !tc_make_map3(&mdo, a.dout, R, groups, R, D, 128) ||
         !tc_make_map3(&mkc, a.K, rows, groups, a.pitch, D, 128) || !tc_make_map3(&mvc, a.V, rows, groups, a.pitch, D, 128) ||
         !tc_make_map3(&mk, a.k, a.T, groups, a.T, D, 128) || !tc_make_map3(&mv, a.v, a.T, groups, a.T, D, 128))
         return cudaErrorInvalidValue;
@@ -733,23 +845,36 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     p.T = a.T;
     p.C = a.C;
     p.n = a.n;
+    p.R = R;
+    p.tiles = dq_tiles(a.Hq, a.Hkv, a.T);
     p.n_mblk = (a.T + 127) / 128;
     p.nbc = (a.n + 127) / 128;
     p.nbC = (a.C + 127) / 128;
     p.scale = 1.f / sqrtf((float)D);
     p.scale_log2 = kLog2e * p.scale;
+    p.parts = dq_parts((int)groups, p.tiles, p.nbc + 1, a.num_sms);
+    const size_t table = groups * p.tiles * 128;
     p.nL2 = a.stats;
-    p.D = a.stats + heads * p.n_mblk * 128;
+    p.D = p.nL2 + table;
+    p.stat = reinterpret_cast<float4*>(p.D + table);
+    p.part = p.stat + table * p.parts;
     p.dq = static_cast<__nv_bfloat16*>(a.dq);
     p.dK = static_cast<__nv_bfloat16*>(a.dK);
     p.dV = static_cast<__nv_bfloat16*>(a.dV);
     p.dk = static_cast<__nv_bfloat16*>(a.dk);
     p.dv = static_cast<__nv_bfloat16*>(a.dv);
     p.wb = a.wb;
-    cudaError_t e = launch_ex(false, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.n_mblk * heads)), dim3(kThreads),
-                              DqCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
+    auto launch_dq = [&](int passes) {
+        p.passes = passes;
+        return launch_ex(false, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.tiles * groups * p.parts)), dim3(kThreads),
+                         DqCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
+    };
+    cudaError_t e = launch_dq(p.parts > 1 ? 1 : 3);
+    if (e == cudaSuccess && p.parts > 1) e = launch_dq(2);
+    if (e == cudaSuccess && p.parts > 1)
+        e = launch_ex(false, ckpt_dq_combine_kernel<D>, dim3((unsigned)(p.tiles * groups * 4)), dim3(256), 0, a.stream, p);
     if (e != cudaSuccess) return e;
-    const int ranks = cluster_for((int)groups, a.Hq / a.Hkv, p.n_mblk, p.nbc, a.num_sms);
+    const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, a.num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.nbC + p.n_mblk) * groups * ranks));
     cfg.blockDim = dim3(kThreads);
@@ -765,6 +890,12 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
 }
 
 }  // namespace
+
+size_t ckpt_stats_floats(const CkptBwdArgs& a) {
+    const int groups = a.B * a.Hkv, tiles = dq_tiles(a.Hq, a.Hkv, a.T);
+    const size_t parts = dq_parts(groups, tiles, (a.n + 127) / 128 + 1, a.num_sms), table = (size_t)groups * tiles * 128;
+    return std::max((size_t)a.B * a.Hq * a.T * 4, table * 2 + (parts > 1 ? parts * table * (4 + a.d) : 0));
+}
 
 cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a) {
     return a.d == 64 ? backward_launch<64>(a) : backward_launch<128>(a);

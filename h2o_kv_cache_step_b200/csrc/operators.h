@@ -87,9 +87,9 @@ struct CkptBwdArgs {
     cudaStream_t stream;
     int num_sms;
 };
-// Statistics of every query row: rows padded to whole 128-row tiles (tensor
-// cores: -log2 of the sum of exponentials, then D), or four floats a row.
-inline size_t ckpt_stats_floats(int B, int Hq, int T) { return (size_t)B * Hq * ((T + 127) / 128 * 128) * 4; }
+// Floats of the workspace for the rows' statistics (and, on the tensor cores, the
+// parts of divided query tiles); needs the sizes, dtype and num_sms of a.
+size_t ckpt_stats_floats(const CkptBwdArgs& a);
 cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a);
 cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a);  // bf16
 

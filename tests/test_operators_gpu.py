@@ -252,6 +252,11 @@ BACKWARDS = [
     (BF16, 1, 2, 1, 64, 1000, 999, 1),
     (BF16, 1, 1, 4, 128, 2000, 1921, 300),
     (BF16, 3, 1, 5, 64, 128, 128, 383),
+    (BF16, 1, 2, 8, 64, 400, 390, 16),    # eight heads in a query tile
+    (BF16, 2, 1, 3, 128, 130, 100, 50),   # heads that end inside a tile
+    (BF16, 1, 1, 1, 128, 4000, 3950, 64), # few tiles, many key blocks
+    (BF16, 1, 1, 2, 64, 3000, 3000, 200),
+    (BF16, 1, 2, 4, 128, 300, 300, 1),
 ]
 
 
