@@ -774,14 +774,22 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     // each CTA adds up its share of the keys over the cluster, in the order of its
     // CTAs; slots n.. of the last cache block get zeros
     const int key0 = cache ? 128 * kb : t0, keys = min(128, (cache ? p.C : p.T) - key0);
-    const int k0 = 128 * rank / ranks, k1 = min(keys, 128 * (rank + 1) / ranks);
-    for (int e = threadIdx.x; e < 2 * (k1 - k0) * (D / 4); e += kThreads) {
-        const int c4 = e % (D / 4), k = k0 + e / (D / 4) % (k1 - k0), part = e / (D / 4) / (k1 - k0);
-        const uint32_t at = sbase + Cfg::OFF_T + ((part * 128 + k) * D + (c4 ^ (k & (D / 4 - 1))) * 4) * 4;
-        float4 a = tc::cluster_load4(at, 0);
-        for (int q = 1; q < ranks; ++q) {
-            const float4 x = tc::cluster_load4(at, q);
-            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+    const int k0 = 128 * rank / ranks, mine = min(keys, 128 * (rank + 1) / ranks) - k0;
+    constexpr int kLanes = D / 4, kPerWarp = 32 / kLanes;  // lanes per row, rows per warp
+    const int c4 = lane % kLanes;
+#pragma unroll 4
+    for (int i = warp * kPerWarp + lane / kLanes; i < 2 * mine; i += kThreads / 32 * kPerWarp) {
+        const int part = i >= mine, k = k0 + i - (part ? mine : 0);
+        const uint32_t at = Cfg::OFF_T + ((part * 128 + k) * D + (c4 ^ (k & (kLanes - 1))) * 4) * 4;
+        float4 a;
+        if (ranks == 1) {
+            a = *reinterpret_cast<const float4*>(smem + at);
+        } else {
+            a = tc::cluster_load4(sbase + at, 0);
+            for (int q = 1; q < ranks; ++q) {
+                const float4 x = tc::cluster_load4(sbase + at, q);
+                a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+            }
         }
         const float mul = part ? p.scale : 1.f;
         uint2 h = make_uint2(tc::pack_bf16(a.x * mul, a.y * mul), tc::pack_bf16(a.z * mul, a.w * mul));
@@ -789,7 +797,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         __nv_bfloat16* base = part ? (cache ? p.dK : p.dk) : (cache ? p.dV : p.dv);
         *reinterpret_cast<uint2*>(base + ((size_t)bg * (cache ? p.C : p.T) + key0 + k) * D + 4 * c4) = h;
     }
-    tc::cluster_sync();  // no CTA leaves while another reads its sums
+    if (ranks > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // CTAs per key block of the dK / dV kernel. A block's query tiles are divided among
