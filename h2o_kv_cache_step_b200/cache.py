@@ -77,7 +77,8 @@ class H2OCache:
                  dtype: torch.dtype = torch.bfloat16, max_T: int | None = None):
         self.B, self.Hq, self.Hkv, self.d, self.C = B, Hq, Hkv, d, C
         self.dtype = dtype
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = torch.cuda.current_device()
+        self.device = torch.device("cuda", self._index)
         h = ctypes.c_void_p()
         rc = lib().h2o_create_ex(B, Hq, Hkv, d, C, _DTYPES[dtype], int(max_T or C), ctypes.byref(h))
         check(rc, None)
@@ -167,8 +168,8 @@ class H2OCache:
     # -- operators next to the step -----------------------------------------
     # (a small call costs as much on the host as on the GPU: pointers and streams go
     # to the library as plain integers)
-    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> int:
-        if t.dtype is not dtype or not t.is_cuda or t.device != self.device or t.shape != shape or not t.is_contiguous():
+    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
@@ -176,7 +177,7 @@ class H2OCache:
     def _on(self, stream, *used) -> int:
         """The stream of a call; its inputs are marked as used there where it is
         not the current one."""
-        current = torch._C._cuda_getCurrentRawStream(self.device.index)
+        current = torch._C._cuda_getCurrentRawStream(self._index)
         if stream is None or stream.cuda_stream == current:
             return current
         if stream.device != self.device:
@@ -210,10 +211,10 @@ class H2OCache:
         if q.dim() != 4:
             raise ValueError("q: need [B, Hq, T, d]")
         B, T = self.B, q.shape[2]
-        args = [self._need("q", q, self.dtype, B, self.Hq, T, self.d),
-                self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
-                self._need("v", v, self.dtype, B, self.Hkv, T, self.d),
-                self._need("parent", parent, torch.int32, B, T)]
+        chunk = (B, self.Hkv, T, self.d)
+        args = [self._need("q", q, self.dtype, (B, self.Hq, T, self.d)), self._need("k", k, self.dtype, chunk),
+                self._need("v", v, self.dtype, chunk),
+                self._need("parent", parent, torch.int32, (B, T))]
         s = self._on(stream, q, k, v, parent)
         (out,) = self._like(stream, q)
         (lse,) = self._empty(stream, torch.float32, q.shape[:3])
@@ -226,9 +227,9 @@ class H2OCache:
         if q.dim() != 4:
             raise ValueError("q: need [B, Hq, T, d]")
         B, T, n = self.B, q.shape[2], self.counters()[1]
-        args = [self._need("q", q, self.dtype, B, self.Hq, T, self.d),
-                self._need("k", k, self.dtype, B, self.Hkv, T, self.d),
-                self._need("v", v, self.dtype, B, self.Hkv, T, self.d)]
+        chunk = (B, self.Hkv, T, self.d)
+        args = [self._need("q", q, self.dtype, (B, self.Hq, T, self.d)), self._need("k", k, self.dtype, chunk),
+                self._need("v", v, self.dtype, chunk)]
         s = self._on(stream, q, k, v)
         nbytes = _record_bytes(B, self.Hq, self.Hkv, self.d, T, n)
         (buf,) = self._empty(stream, torch.uint8, (nbytes,))
@@ -256,7 +257,7 @@ class H2OCache:
         checkpoint stands for: (dq, dK, dV, dk, dv) in the cache's type, dK and
         dV over the C slots. The cache itself is not read."""
         rec = self._record(ck)
-        do = self._need("dout", dout, self.dtype, self.B, self.Hq, ck.T, self.d)
+        do = self._need("dout", dout, self.dtype, (self.B, self.Hq, ck.T, self.d))
         s = self._on(stream, ck.buffer, dout)
         chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
         g = self._like(stream, dout) + self._empty(stream, self.dtype, cache, cache, chunk, chunk)
@@ -276,11 +277,11 @@ class H2OCache:
             raise ValueError("token_slots: need [B, Hkv, T]")
         T = token_slots.shape[2]
         cache, chunk = (self.B, self.Hkv, self.C, self.d), (self.B, self.Hkv, T, self.d)
-        args = [self._need("token_slots", token_slots, torch.int32, self.B, self.Hkv, T), T, int(n),
-                self._need("dK", dK, self.dtype, *cache), self._need("dV", dV, self.dtype, *cache),
-                self._need("dk", dk, self.dtype, *chunk), self._need("dv", dv, self.dtype, *chunk)]
+        args = [self._need("token_slots", token_slots, torch.int32, chunk[:3]), T, int(n),
+                self._need("dK", dK, self.dtype, cache), self._need("dV", dV, self.dtype, cache),
+                self._need("dk", dk, self.dtype, chunk), self._need("dv", dv, self.dtype, chunk)]
         for name, t in (("gK_next", gK_next), ("gV_next", gV_next)):
-            args.append(None if t is None else self._need(name, t, torch.float32, *cache))
+            args.append(None if t is None else self._need(name, t, torch.float32, cache))
         s = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
         g = (self._empty(stream, torch.float32, cache, cache) if gK_next is None else self._like(stream, gK_next, gK_next)) \
             + self._like(stream, dk, dv)

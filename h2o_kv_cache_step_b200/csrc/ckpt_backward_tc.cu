@@ -10,8 +10,12 @@
 //     The first computes S = Q K^T and dP = dO V^T and keeps each row's running
 //     maximum m, sum l = sum e and w = sum e dp (e = 2^(s - m)); then
 //     LSE = m + log2 l and D = w / l, in fp32. The second recomputes both products,
-//     writes dS = P (dP - D) as bf16 over S in TMEM and accumulates dQ += dS K with
-//     dS as the A operand from TMEM. Where tiles are few, their blocks are divided
+//     writes dS = P (dP - D) over S in TMEM as a bf16 pair hi + lo and accumulates
+//     dQ += hi K + lo K with them as A operands from TMEM: the terms of dq cancel
+//     (sum_j ds_j = 0, and keys have much in common), so 8 bits of dS would cost
+//     it 1.7 times the rounding of the result (in 2-norm, heavy-hitter keys; dk and
+//     dv, whose terms cancel less, stay within 1.45 times with one bf16 each). The
+//     second product is 18 us of 121 at T=1024 C=2048. Where tiles are few, their blocks are divided
 //     among several CTAs: one launch for the first pass, one for the second, and
 //     ckpt_dq_combine_kernel adds up the parts in order.
 // ckpt_dkdv_tc_kernel  one CTA, or a cluster, per (KV head, 128-key block), one key
@@ -19,7 +23,7 @@
 //     P^T and dS^T go back over them as bf16 and are the A operands of
 //     dV += P^T dO and dK += dS^T Q.
 //
-// Bound by the tensor core: 5 products of 2 d per visible (row, key) in the
+// Bound by the tensor core: 6 products of 2 d per visible (row, key) in the
 // first kernel, 4 in the second. An operand pair from shared memory needs
 // 128 bytes a clock at the MMA's full rate, all there is, so P and dS stay in
 // TMEM (64 bytes a clock), and they never cross shared memory. Ten warps: a TMA
@@ -29,8 +33,8 @@
 // computed, dK(t), dP(t+1) while P(t+1) is.
 //
 // Rows past the end of a KV head or cache arrive as zeros (3-D tensor maps), so
-// nothing of another head enters a tile. P and dS are rounded to bf16, the MMA's
-// operand type; statistics and gradients accumulate in fp32.
+// nothing of another head enters a tile. The MMA's operands are bf16; statistics
+// and gradients accumulate in fp32.
 #include <cuda.h>
 #include <math.h>
 
@@ -254,9 +258,12 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             const int ks = (L0 + 2 * t) % RING;
             const uint64_t b = dRingN + (uint64_t)((ks * Cfg::TILE) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 keys at a time; the keys' halves at columns 0 and 64
-                tc::mma_bf16_ts_warp(tmem + 384, tmem + 128 * (t & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
-                                     b + (uint64_t)((kk * 16 * 128) >> 4), Cfg::IDESC_G, (t > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {  // 16 keys at a time; the keys' halves at columns 0 and 64, each hi and lo
+                const uint32_t a = tmem + 128 * (t & 1) + 64 * (kk >> 2) + 8 * (kk & 3);
+                const uint64_t bk = b + (uint64_t)((kk * 16 * 128) >> 4);
+                tc::mma_bf16_ts_warp(tmem + 384, a, bk, Cfg::IDESC_G, (t > 0 || kk > 0) ? 1u : 0u);
+                tc::mma_bf16_ts_warp(tmem + 384, a + 32, bk, Cfg::IDESC_G, 1u);
+            }
             tc::mma_commit_warp(ring_empty + ks);
             if (t + 2 < n2) ok = issue_s(t + 2);
         }
@@ -398,20 +405,23 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             }
             if (!(ok = warp_wait(dp_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
-            uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t dp[32];
+                uint32_t dp[32], hi[16], lo[16];
                 tc::tmem_ld32(tl + 256 + 32 * c, dp);
                 tc::tmem_ld_wait();
                 tc::reg_fence(dp);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float2 y = tc::fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd2);
-                    pk[16 * c + (e >> 1)] = tc::pack_bf16(__uint_as_float(s[c][e]) * y.x, __uint_as_float(s[c][e + 1]) * y.y);
+                    const float a = __uint_as_float(s[c][e]) * y.x, b = __uint_as_float(s[c][e + 1]) * y.y;
+                    const uint32_t h = tc::pack_bf16(a, b);
+                    hi[e >> 1] = h;
+                    lo[e >> 1] = tc::pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
                 }
+                tc::tmem_st16(tS + 16 * c, hi);
+                tc::tmem_st16(tS + 32 + 16 * c, lo);
             }
-            tc::tmem_st32(tS, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();

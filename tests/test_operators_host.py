@@ -37,7 +37,7 @@ def test_constants_match_the_header():
 class _Never:
     """Stands in for a context that no refused call may reach."""
     B, Hq, Hkv, d, C, dtype = 2, 4, 2, 64, 32, torch.bfloat16
-    device = torch.device("cuda", 0)
+    device, _index = torch.device("cuda", 0), 0
     _need = H2OCache._need
     _record = H2OCache._record
 
