@@ -157,11 +157,20 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    const uint32_t tmem = *tmem_slot;  // S of the two buffers at 0 and 128, dP at 256 (and 384 in pass 1), dQ at 384
+    uint32_t tmem = 0;
+    if (warp == 0) {
+        // the loader has initialised the barriers and needs nothing else: its first loads
+        // are on their way while the others set up
+        __syncwarp();
+        tc::named_arrive(4, kThreads);
+    } else {
+        if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+        fence_before_sync();
+        tc::named_sync(4, kThreads);
+        fence_after_sync();
+        tmem = *tmem_slot;
+    }
+     // S of the two buffers at 0 and 128, dP at 256 (and 384 in pass 1), dQ at 384
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == 0) {
@@ -578,11 +587,20 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    const uint32_t tmem = *tmem_slot;  // S^T at 0, dP^T at 128, dV at 256, dK at 256 + D
+    uint32_t tmem = 0;
+    if (warp == 0) {
+        // the loader has initialised the barriers and needs nothing else: its first loads
+        // are on their way while the others set up
+        __syncwarp();
+        tc::named_arrive(4, kThreads);
+    } else {
+        if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+        fence_before_sync();
+        tc::named_sync(4, kThreads);
+        fence_after_sync();
+        tmem = *tmem_slot;
+    }
+     // S^T at 0, dP^T at 128, dV at 256, dK at 256 + D
     const uint32_t sbase = smem_u32(smem);
 
     if (warp == 0) {

@@ -133,7 +133,7 @@ __device__ __forceinline__ void merge_row(const TreeParams& p, unsigned bg, int 
     const bool second = p.split.first(c0) < b0;
     auto part = [&](int c) { return (size_t)(2 * c + (c == c0 && second ? 1 : 0)); };
     const int r = row % kUnitRows;
-    constexpr int kBatch = 8;  // parts in flight: one after the other they cost an L2 latency each
+    constexpr int kBatch = 9;  // parts in flight: one after the other they cost an L2 latency each
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     bool absent = false;
@@ -221,11 +221,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    const uint32_t tmem = *tmem_slot;  // tile X: S at 256 X, O at 256 X + 128
+    uint32_t tmem = 0;  // tile X: S at 256 X, O at 256 X + 128
+    if (warp == 0) {
+        // the loader has initialised the barriers and needs nothing else: its first loads
+        // are on their way while the others set up
+        __syncwarp();
+        tc::named_arrive(4, Cfg::THREADS);
+    } else {
+        if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+        fence_before_sync();
+        tc::named_sync(4, Cfg::THREADS);
+        fence_after_sync();
+        tmem = *tmem_slot;
+    }
     const uint32_t sbase = smem_u32(smem);
     griddep_launch_dependents();  // the merge waits for this grid's end before it reads
 
