@@ -141,6 +141,28 @@ def test_tree_bad_slots_and_queries_are_not_hidden():
         assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("steps", [(0, 20, 21, 60, 61), (0, -90, 15, 200, 199, 500), (300, 0, -300, 310, 400)])
+@pytest.mark.parametrize("T", [2, 70])
+def test_tree_scores_that_jump_along_the_cache(steps, T):
+    """Logits that rise and fall by tens and hundreds of powers of two from one
+    128-slot block to the next: the running maximum moves late, at once, or not."""
+    G, d, n = 2, 64, 128 * len(steps) - 30
+    q, k, v, K, V = heads(BF16, 1, 1, G, d, 128 * len(steps), n, T, seed=12)
+    q[:, 1, :, 0] *= -1
+    q[..., 0] = torch.where(q[..., 0] < 0, -1.0, 1.0)
+    for i, s in enumerate(steps):  # s powers of two in the first channel, for the rows with a 1 there
+        K[:, :, 128 * i:128 * (i + 1), 0] = s * math.log(2) * math.sqrt(d)
+    K[:, :, n:] = 0
+    parent = trees(1, T)
+    c = cache_of(K, V, G, n)
+    out, lse = c.tree_attend(q, k, v, parent)
+    want, wlse, bound, lbound = ref.tree(q, k, v, parent, K, V, n, BF16)
+    there = wlse > -math.inf
+    ref.within("out", out, want, bound)
+    ref.within("lse", lse[there], wlse[there], lbound[there])
+    assert torch.equal(out, c.tree_attend(q, k, v, parent)[0])
+
+
 @pytest.mark.parametrize("T", [3, 100])
 def test_tree_with_no_node_in_it(T):
     q, k, v, K, V = heads(BF16, 2, 2, 2, 64, 256, 200, T)
