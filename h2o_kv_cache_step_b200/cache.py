@@ -5,6 +5,7 @@ current CUDA stream; every computation happens in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -22,6 +23,14 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
 
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _new_on(stream):
+    """Where a call's new tensors are made: they belong to its stream."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _record_bytes(B: int, Hq: int, Hkv: int, d: int, T: int, n: int) -> int:
@@ -83,6 +92,7 @@ class H2OCache:
         rc = lib().h2o_create_ex(B, Hq, Hkv, d, C, _DTYPES[dtype], int(max_T or C), ctypes.byref(h))
         check(rc, None)
         self._h = h
+        self._P, self._n = ctypes.c_int64(), ctypes.c_int64()  # what counters() reads into
 
     # -- lifetime -----------------------------------------------------------
     def close(self) -> None:
@@ -187,20 +197,6 @@ class H2OCache:
                 t.record_stream(stream)
         return stream.cuda_stream
 
-    def _empty(self, stream, dtype: torch.dtype, *shapes):
-        """New tensors that belong to the stream of the call."""
-        if stream is None:
-            return [torch.empty(*x, dtype=dtype, device=self.device) for x in shapes]
-        with torch.cuda.stream(stream):
-            return [torch.empty(*x, dtype=dtype, device=self.device) for x in shapes]
-
-    def _like(self, stream, *tensors: torch.Tensor):
-        """As _empty, of the types and shapes of (contiguous) tensors."""
-        if stream is None:
-            return [torch.empty_like(t) for t in tensors]
-        with torch.cuda.stream(stream):
-            return [torch.empty_like(t) for t in tensors]
-
     def tree_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent: torch.Tensor, stream=None):
         """Attention of a tree of T drafted tokens per sequence over the cache,
         which stays as it is. q [B,Hq,T,d], k and v [B,Hkv,T,d], parent int32
@@ -216,8 +212,9 @@ class H2OCache:
                 self._need("v", v, self.dtype, chunk),
                 self._need("parent", parent, torch.int32, (B, T))]
         s = self._on(stream, q, k, v, parent)
-        (out,) = self._like(stream, q)
-        (lse,) = self._empty(stream, torch.float32, q.shape[:3])
+        with _new_on(stream):
+            out = torch.empty_like(q)
+            lse = torch.empty(B, self.Hq, T, dtype=torch.float32, device=self.device)
         self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, s))
         return out, lse
 
@@ -232,7 +229,8 @@ class H2OCache:
                 self._need("v", v, self.dtype, chunk)]
         s = self._on(stream, q, k, v)
         nbytes = _record_bytes(B, self.Hq, self.Hkv, self.d, T, n)
-        (buf,) = self._empty(stream, torch.uint8, (nbytes,))
+        with _new_on(stream):
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self._check(lib().h2o_checkpoint_save(self._h, *args, T, buf.data_ptr(), nbytes, s))
         return H2OCheckpoint(buf, B, self.Hq, self.Hkv, self.d, T, n)
 
@@ -247,10 +245,15 @@ class H2OCache:
         C slots with zeros in the empty ones. The cache itself is not changed."""
         rec = self._record(ck)
         s = self._on(stream, ck.buffer)
-        chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
-        x = self._empty(stream, self.dtype, (self.B, self.Hq, ck.T, self.d), chunk, chunk, cache, cache)
-        self._check(lib().h2o_checkpoint_restore(self._h, *rec, *[t.data_ptr() for t in x], s))
-        return tuple(x)
+        new = dict(dtype=self.dtype, device=self.device)
+        with _new_on(stream):
+            q = torch.empty(self.B, self.Hq, ck.T, self.d, **new)
+            k = torch.empty(self.B, self.Hkv, ck.T, self.d, **new)
+            K = torch.empty(self.B, self.Hkv, self.C, self.d, **new)
+            v, V = torch.empty_like(k), torch.empty_like(K)
+        self._check(lib().h2o_checkpoint_restore(self._h, *rec, q.data_ptr(), k.data_ptr(), v.data_ptr(), K.data_ptr(),
+                                                 V.data_ptr(), s))
+        return q, k, v, K, V
 
     def checkpoint_backward(self, ck: H2OCheckpoint, dout: torch.Tensor, stream=None):
         """Gradients of the checkpointed step's attention at the values the
@@ -259,10 +262,15 @@ class H2OCache:
         rec = self._record(ck)
         do = self._need("dout", dout, self.dtype, (self.B, self.Hq, ck.T, self.d))
         s = self._on(stream, ck.buffer, dout)
-        chunk, cache = (self.B, self.Hkv, ck.T, self.d), (self.B, self.Hkv, self.C, self.d)
-        g = self._like(stream, dout) + self._empty(stream, self.dtype, cache, cache, chunk, chunk)
-        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, *[t.data_ptr() for t in g], s))
-        return tuple(g)
+        new = dict(dtype=self.dtype, device=self.device)
+        with _new_on(stream):
+            dq = torch.empty_like(dout)
+            dK = torch.empty(self.B, self.Hkv, self.C, self.d, **new)
+            dk = torch.empty(self.B, self.Hkv, ck.T, self.d, **new)
+            dV, dv = torch.empty_like(dK), torch.empty_like(dk)
+        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, dq.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+                                                  dk.data_ptr(), dv.data_ptr(), s))
+        return dq, dK, dV, dk, dv
 
     def carry_grad(self, token_slots: torch.Tensor, n: int, dK: torch.Tensor, dV: torch.Tensor, dk: torch.Tensor,
                    dv: torch.Tensor, gK_next: torch.Tensor | None = None, gV_next: torch.Tensor | None = None,
@@ -277,16 +285,18 @@ class H2OCache:
             raise ValueError("token_slots: need [B, Hkv, T]")
         T = token_slots.shape[2]
         cache, chunk = (self.B, self.Hkv, self.C, self.d), (self.B, self.Hkv, T, self.d)
-        args = [self._need("token_slots", token_slots, torch.int32, chunk[:3]), T, int(n),
-                self._need("dK", dK, self.dtype, cache), self._need("dV", dV, self.dtype, cache),
-                self._need("dk", dk, self.dtype, chunk), self._need("dv", dv, self.dtype, chunk)]
-        for name, t in (("gK_next", gK_next), ("gV_next", gV_next)):
-            args.append(None if t is None else self._need(name, t, torch.float32, cache))
+        slots = self._need("token_slots", token_slots, torch.int32, chunk[:3])
+        own = (self._need("dK", dK, self.dtype, cache), self._need("dV", dV, self.dtype, cache),
+               self._need("dk", dk, self.dtype, chunk), self._need("dv", dv, self.dtype, chunk))
+        later = (None if gK_next is None else self._need("gK_next", gK_next, torch.float32, cache),
+                 None if gV_next is None else self._need("gV_next", gV_next, torch.float32, cache))
         s = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
-        g = (self._empty(stream, torch.float32, cache, cache) if gK_next is None else self._like(stream, gK_next, gK_next)) \
-            + self._like(stream, dk, dv)
-        self._check(lib().h2o_carry_grad(self._h, *args, *[t.data_ptr() for t in g], s))
-        return tuple(g)
+        with _new_on(stream):
+            gK = torch.empty(*cache, dtype=torch.float32, device=self.device)
+            gV, gk, gv = torch.empty_like(gK), torch.empty_like(dk), torch.empty_like(dv)
+        self._check(lib().h2o_carry_grad(self._h, slots, T, int(n), *own, *later, gK.data_ptr(), gV.data_ptr(),
+                                         gk.data_ptr(), gv.data_ptr(), s))
+        return gK, gV, gk, gv
 
     def set_policy(self, policy: int) -> None:
         """Eviction ranking for the following steps: _lib.H2O_POLICY_SUM (the
@@ -327,9 +337,8 @@ class H2OCache:
 
     # -- inspection ---------------------------------------------------------
     def counters(self) -> tuple[int, int]:
-        P, n = ctypes.c_int64(), ctypes.c_int64()
-        self._check(lib().h2o_counters(self._h, ctypes.byref(P), ctypes.byref(n)))
-        return P.value, n.value
+        self._check(lib().h2o_counters(self._h, self._P, self._n))
+        return self._P.value, self._n.value
 
     def scores(self, stream=None) -> torch.Tensor:
         dst = torch.empty((self.B, self.Hkv, self.C), dtype=torch.float32, device=self.device)

@@ -19,8 +19,9 @@ namespace h2o {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = 2;  // dq: query rows per CTA, in registers
-constexpr int kKeys = 2;  // dk, dv: keys per CTA, in registers
+// dq: query rows per CTA, and dk, dv: keys per CTA, in registers: two where that still
+// gives every SM two CTAs, one otherwise (64 rows, 320 keys, 4 / 2 heads: dq 9.6 us with
+// two and 8.0 with one, dk and dv 6.3 and 8.1).
 
 __device__ __forceinline__ float sum8(float x) {  // over the eight lanes of a key or row
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -39,7 +40,7 @@ __device__ __forceinline__ float4 sum_subs(float4 a) {
 // statistics. One pass over the keys with a running maximum, keeping
 // A = sum e dp k, Z = sum e k, sum e dp and sum e (e = exp(s - max)):
 // dq = (A - D Z) / (sum e sqrt(d)). Eight lanes share a key.
-template <typename E, int D>
+template <typename E, int D, int kRows>
 __global__ void __launch_bounds__(kWarps * 32)
 ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
                     const E* __restrict__ V, const E* __restrict__ dout, E* __restrict__ dq, float4* __restrict__ stats,
@@ -150,7 +151,7 @@ ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* _
 // dk and dv of kKeys keys of one KV group: key u < C is cache slot u (zero
 // gradients from n on), u >= C is chunk token u - C. Eight lanes share a query
 // row, the CTA takes 32 rows at a time.
-template <typename E, int D>
+template <typename E, int D, int kKeys>
 __global__ void __launch_bounds__(kWarps * 32)
 ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
                       const E* __restrict__ V, const E* __restrict__ dout, const float4* __restrict__ stats,
@@ -239,22 +240,32 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
     }
 }
 
+template <typename E, int D, int kRows>
+cudaError_t dq_launch(const CkptBwdArgs& a, float scale) {
+    const int G = a.Hq / a.Hkv, per = (G * a.T + kRows - 1) / kRows;
+    ckpt_dq_simt_kernel<E, D, kRows><<<a.B * a.Hkv * per, kWarps * 32, 0, a.stream>>>(
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq,
+        reinterpret_cast<float4*>(a.stats), G, a.T, a.n, a.pitch, per, kLog2e * scale, scale);
+    return cudaGetLastError();
+}
+
+template <typename E, int D, int kKeys>
+cudaError_t dkdv_launch(const CkptBwdArgs& a, float scale) {
+    const int G = a.Hq / a.Hkv, per = (a.C + a.T + kKeys - 1) / kKeys;
+    ckpt_dkdv_simt_kernel<E, D, kKeys><<<a.B * a.Hkv * per, kWarps * 32, 0, a.stream>>>(
+        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
+        reinterpret_cast<const float4*>(a.stats), (E*)a.dK, (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n, a.pitch, per,
+        kLog2e * scale, scale);
+    return cudaGetLastError();
+}
+
 template <typename E, int D>
 cudaError_t backward_typed(const CkptBwdArgs& a) {
-    const float scale = 1.f / sqrtf((float)D), scale_log2 = kLog2e * scale;
-    const int G = a.Hq / a.Hkv, groups = a.B * a.Hkv;
-    const int rows = (G * a.T + kRows - 1) / kRows, keys = (a.C + a.T + kKeys - 1) / kKeys;
-    ckpt_dq_simt_kernel<E, D><<<groups * rows, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq,
-        reinterpret_cast<float4*>(a.stats), G,
-        a.T, a.n, a.pitch, rows, scale_log2, scale);
-    cudaError_t e = cudaGetLastError();
+    const float scale = 1.f / sqrtf((float)D);
+    const long long ctas = 4ll * a.num_sms;
+    const cudaError_t e = (long long)a.B * a.Hq * a.T >= ctas ? dq_launch<E, D, 2>(a, scale) : dq_launch<E, D, 1>(a, scale);
     if (e != cudaSuccess) return e;
-    ckpt_dkdv_simt_kernel<E, D><<<groups * keys, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
-        reinterpret_cast<const float4*>(a.stats), (E*)a.dK,
-        (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n, a.pitch, keys, scale_log2, scale);
-    return cudaGetLastError();
+    return (long long)a.B * a.Hkv * (a.C + a.T) >= ctas ? dkdv_launch<E, D, 2>(a, scale) : dkdv_launch<E, D, 1>(a, scale);
 }
 
 }  // namespace
