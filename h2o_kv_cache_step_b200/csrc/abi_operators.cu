@@ -103,16 +103,17 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     if ((reinterpret_cast<uintptr_t>(parent) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3))
         return fail(c, H2O_ERR_ALIGN, "parent and lse must be 4-byte aligned");
     DeviceGuard g(c->device);
-    if (c->use_tc && !c->tree_part) {
+    if (!c->tree_part) {
         if (capturing((cudaStream_t)stream))
             return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
-        const size_t words = (size_t)c->B * c->Hkv;
+        const size_t words = std::max((size_t)c->B * c->Hkv, (size_t)c->num_sms);
         if (!c->tree_count) {
             H2O_TRY(c, cudaMalloc(&c->tree_count, sizeof(unsigned) * words), "cudaMalloc(tree workspace)");
             H2O_TRY(c, cudaMemset(c->tree_count, 0, sizeof(unsigned) * words), "cudaMemset(tree workspace)");
             H2O_TRY(c, cudaStreamSynchronize(nullptr), "cudaMemset(tree workspace)");
         }
-        H2O_TRY(c, cudaMalloc(&c->tree_part, sizeof(float) * tree_part_floats(c->num_sms, c->d)), "cudaMalloc(tree workspace)");
+        const size_t floats = c->use_tc ? tree_part_floats(c->num_sms, c->d) : tree_simt_part_floats(c->num_sms, c->d);
+        H2O_TRY(c, cudaMalloc(&c->tree_part, sizeof(float) * floats), "cudaMalloc(tree workspace)");
     }
     TreeArgs a{};
     a.B = c->B;
@@ -137,7 +138,8 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     a.wb.ns = c->wait_ns;
     a.stream = (cudaStream_t)stream;
     a.num_sms = c->num_sms;
-    H2O_TRY(c, c->use_tc ? launch_tree_tc(a) : launch_tree_simt(a), "launch tree attention");
+    const bool tc = c->use_tc && (long long)c->B * c->Hq * T * (c->n + T) * c->d > kTreeSimtProducts;
+    H2O_TRY(c, tc ? launch_tree_tc(a) : launch_tree_simt(a), "launch tree attention");
     return H2O_OK;
 }
 

@@ -28,8 +28,8 @@ struct TreeArgs {
     const void* Vc;         // [B,Hkv,C,d]
     void* out;              // [B,Hq,T,d]
     float* lse;             // [B,Hq,T]
-    float* part;            // tensor cores: workspace of tree_part_floats() floats
-    unsigned* count;        // tensor cores: workspace of B * Hkv words, zero between calls
+    float* part;            // workspace of tree_part_floats() floats (CUDA cores: tree_simt_part_floats())
+    unsigned* count;        // workspace of max(B * Hkv, num_sms) words, zero between calls
     WaitBound wb;
     cudaStream_t stream;
     int num_sms;
@@ -37,6 +37,12 @@ struct TreeArgs {
 cudaError_t launch_tree_simt(const TreeArgs& a);
 cudaError_t launch_tree_tc(const TreeArgs& a);  // bf16
 size_t tree_part_floats(int num_sms, int d);
+size_t tree_simt_part_floats(int num_sms, int d);
+// bf16: up to so many products of a query and a key channel take the CUDA cores, where
+// the tensor-core kernel's way through TMEM costs more than the arithmetic. Measured,
+// us on the device, CUDA cores / tensor cores: 0.05 million 5.6 / 8.8, 0.7 million
+// 6.1 / 8.6, 8.4 million 10.9 / 12.7, 16.8 million 15.0 / 12.6, 67 million 34.4 / 24.5.
+constexpr long long kTreeSimtProducts = 10ll << 20;
 
 // 8-bit record of a step's inputs: codes of q, k, v (the chunk) and of the n
 // valid slots of K and V, row after row, then their scales in the same order.

@@ -72,6 +72,16 @@ TREES = [
     (BF16, 1, 2, 4, 64, 4000, 3999, 255),
     (BF16, 1, 2, 8, 128, 5000, 4097, 256),
     (BF16, 2, 1, 1, 128, 40, 33, 256),    # a tree longer than the cache
+    # the same kinds with enough work for the tensor cores
+    (BF16, 4, 8, 4, 128, 1000, 997, 1),
+    (BF16, 8, 8, 2, 64, 700, 641, 3),
+    (BF16, 8, 4, 3, 64, 129, 128, 43),
+    (BF16, 7, 8, 1, 128, 1500, 1409, 1),
+    (BF16, 8, 8, 3, 128, 300, 0, 77),
+    (BF16, 16, 4, 1, 128, 40, 33, 256),
+    (BF16, 2, 4, 1, 128, 16384, 16383, 5),
+    (FP32, 1, 1, 2, 64, 3000, 2990, 1),   # fp32, the keys divided
+    (FP32, 1, 2, 4, 128, 900, 899, 2),
 ]
 
 
@@ -95,9 +105,10 @@ def test_tree_attention(dtype, B, Hkv, G, d, C, n, T):
         assert torch.equal(a, b) if torch.is_tensor(a) else a == b
 
 
-@pytest.mark.parametrize("dtype,G,d,n,T", [(FP32, 2, 64, 70, 12), (BF16, 4, 128, 700, 3), (BF16, 4, 128, 700, 40), (BF16, 2, 64, 130, 200)])
-def test_tree_keys_that_a_row_does_not_see_leave_it_alone(dtype, G, d, n, T):
-    B, Hkv, C = 2, 2, 800
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,n,T", [(FP32, 2, 2, 2, 64, 70, 12), (BF16, 2, 2, 4, 128, 700, 3), (BF16, 2, 2, 4, 128, 700, 40),
+                                                  (BF16, 2, 2, 2, 64, 130, 200), (BF16, 8, 8, 4, 128, 700, 3)])
+def test_tree_keys_that_a_row_does_not_see_leave_it_alone(dtype, B, Hkv, G, d, n, T):
+    C = 800
     q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=5)
     parent = trees(B, T, seed=6)
     clean = cache_of(K, V, Hkv * G, n).tree_attend(q, k, v, parent)
@@ -120,7 +131,7 @@ def test_tree_keys_that_a_row_does_not_see_leave_it_alone(dtype, G, d, n, T):
 def test_tree_bad_slots_and_queries_are_not_hidden():
     """A NaN in a valid slot reaches every row of its KV head, one in a query its
     own row; an infinite logit is NaN as in the definition."""
-    for T in (1, 40):
+    for T in (1, 9, 60):
         q, k, v, K, V = heads(BF16, 1, 2, 4, 128, 512, 512, T, seed=2)
         parent = trees(1, T, absent=False)
         clean = cache_of(K, V, 8, 512).tree_attend(q, k, v, parent)[0]
@@ -142,18 +153,18 @@ def test_tree_bad_slots_and_queries_are_not_hidden():
 
 
 @pytest.mark.parametrize("steps", [(0, 20, 21, 60, 61), (0, -90, 15, 200, 199, 500), (300, 0, -300, 310, 400)])
-@pytest.mark.parametrize("T", [2, 70])
-def test_tree_scores_that_jump_along_the_cache(steps, T):
+@pytest.mark.parametrize("B,T", [(1, 2), (1, 70), (5, 70)])
+def test_tree_scores_that_jump_along_the_cache(steps, B, T):
     """Logits that rise and fall by tens and hundreds of powers of two from one
     128-slot block to the next: the running maximum moves late, at once, or not."""
     G, d, n = 2, 64, 128 * len(steps) - 30
-    q, k, v, K, V = heads(BF16, 1, 1, G, d, 128 * len(steps), n, T, seed=12)
+    q, k, v, K, V = heads(BF16, B, 1, G, d, 128 * len(steps), n, T, seed=12)
     q[:, 1, :, 0] *= -1
     q[..., 0] = torch.where(q[..., 0] < 0, -1.0, 1.0)
     for i, s in enumerate(steps):  # s powers of two in the first channel, for the rows with a 1 there
         K[:, :, 128 * i:128 * (i + 1), 0] = s * math.log(2) * math.sqrt(d)
     K[:, :, n:] = 0
-    parent = trees(1, T)
+    parent = trees(B, T)
     c = cache_of(K, V, G, n)
     out, lse = c.tree_attend(q, k, v, parent)
     want, wlse, bound, lbound = ref.tree(q, k, v, parent, K, V, n, BF16)
@@ -163,10 +174,10 @@ def test_tree_scores_that_jump_along_the_cache(steps, T):
     assert torch.equal(out, c.tree_attend(q, k, v, parent)[0])
 
 
-@pytest.mark.parametrize("T", [3, 100])
-def test_tree_with_no_node_in_it(T):
-    q, k, v, K, V = heads(BF16, 2, 2, 2, 64, 256, 200, T)
-    parent = torch.full((2, T), -2, dtype=torch.int32, device="cuda")
+@pytest.mark.parametrize("B,T", [(2, 3), (2, 100), (16, 100)])
+def test_tree_with_no_node_in_it(B, T):
+    q, k, v, K, V = heads(BF16, B, 2, 2, 64, 256, 200, T)
+    parent = torch.full((B, T), -2, dtype=torch.int32, device="cuda")
     parent[0, 1:] = 0                      # under an absent node: absent too
     out, lse = cache_of(K, V, 4, 200).tree_attend(q, k, v, parent)
     assert not out.any() and (lse == -math.inf).all()
