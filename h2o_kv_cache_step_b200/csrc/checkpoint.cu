@@ -169,6 +169,7 @@ ckpt_save_kernel(const __grid_constant__ Sections sec, int8_t* __restrict__ code
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads)
 ckpt_restore_kernel(const __grid_constant__ Sections sec, const int8_t* __restrict__ codes, const float* __restrict__ scales) {
+    griddep_launch_dependents();  // the backward's first kernel waits for this grid's end before it reads
     const Place p = place<D>(sec);
     if (!p.in || p.x == nullptr) return;
     float f[kPer] = {};

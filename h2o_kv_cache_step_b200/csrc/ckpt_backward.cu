@@ -12,6 +12,7 @@
 // saw, so its log-sum-exp would not normalise these weights.
 #include <math.h>
 
+#include "kernels.h"
 #include "operators.h"
 #include "vec.cuh"
 
@@ -45,6 +46,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
                     const E* __restrict__ V, const E* __restrict__ dout, E* __restrict__ dq, float4* __restrict__ stats,
                     int G, int T, int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+    griddep_wait();  // the restored values are there
+    griddep_launch_dependents();
     constexpr int Q4 = D / 32;
     __shared__ float4 part[2][kWarps][kRows][D / 4];
     __shared__ float part_s[kWarps][kRows][3];  // maximum, sum e, sum e dp
@@ -157,6 +160,7 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
                       const E* __restrict__ V, const E* __restrict__ dout, const float4* __restrict__ stats,
                       E* __restrict__ dK, E* __restrict__ dV, E* __restrict__ dk, E* __restrict__ dv, int G, int C, int T,
                       int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+    griddep_wait();  // the statistics are there
     constexpr int Q4 = D / 32;
     __shared__ float4 part[2][kWarps][kKeys][D / 4];
     const int R = G * T;
@@ -243,20 +247,18 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
 template <typename E, int D, int kRows>
 cudaError_t dq_launch(const CkptBwdArgs& a, float scale) {
     const int G = a.Hq / a.Hkv, per = (G * a.T + kRows - 1) / kRows;
-    ckpt_dq_simt_kernel<E, D, kRows><<<a.B * a.Hkv * per, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout, (E*)a.dq,
-        reinterpret_cast<float4*>(a.stats), G, a.T, a.n, a.pitch, per, kLog2e * scale, scale);
-    return cudaGetLastError();
+    return launch_ex(true, ckpt_dq_simt_kernel<E, D, kRows>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
+                     a.stream, (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
+                     (E*)a.dq, reinterpret_cast<float4*>(a.stats), G, a.T, a.n, a.pitch, per, kLog2e * scale, scale);
 }
 
 template <typename E, int D, int kKeys>
 cudaError_t dkdv_launch(const CkptBwdArgs& a, float scale) {
     const int G = a.Hq / a.Hkv, per = (a.C + a.T + kKeys - 1) / kKeys;
-    ckpt_dkdv_simt_kernel<E, D, kKeys><<<a.B * a.Hkv * per, kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
-        reinterpret_cast<const float4*>(a.stats), (E*)a.dK, (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n, a.pitch, per,
-        kLog2e * scale, scale);
-    return cudaGetLastError();
+    return launch_ex(true, ckpt_dkdv_simt_kernel<E, D, kKeys>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
+                     a.stream, (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
+                     reinterpret_cast<const float4*>(a.stats), (E*)a.dK, (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n,
+                     a.pitch, per, kLog2e * scale, scale);
 }
 
 template <typename E, int D>

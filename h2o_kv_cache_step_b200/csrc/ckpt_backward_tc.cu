@@ -170,6 +170,8 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         fence_after_sync();
         tmem = *tmem_slot;
     }
+    griddep_wait();  // the kernel before has written what this one reads
+    griddep_launch_dependents();
      // S of the two buffers at 0 and 128, dP at 256 (and 384 in pass 1), dQ at 384
     const uint32_t sbase = smem_u32(smem);
 
@@ -487,6 +489,8 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
 // neighbouring lanes neighbouring rows, as the parts lie.
 template <int D>
 __global__ void __launch_bounds__(256) ckpt_dq_combine_kernel(const CkptTcParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
     const int r = threadIdx.x % 32 + 32 * (blockIdx.x % 4), unit = blockIdx.x / 4;  // KV head and tile
     const int row = unit % p.tiles * 128 + r;
     if (row >= p.R) return;
@@ -600,6 +604,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         fence_after_sync();
         tmem = *tmem_slot;
     }
+    griddep_wait();  // the kernel before has written what this one reads
      // S^T at 0, dP^T at 128, dV at 256, dK at 256 + D
     const uint32_t sbase = smem_u32(smem);
 
@@ -902,13 +907,13 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     p.wb = a.wb;
     auto launch_dq = [&](int passes) {
         p.passes = passes;
-        return launch_ex(false, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.tiles * groups * p.parts)), dim3(kThreads),
+        return launch_ex(true, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.tiles * groups * p.parts)), dim3(kThreads),
                          DqCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
     };
     cudaError_t e = launch_dq(p.parts > 1 ? 1 : 3);
     if (e == cudaSuccess && p.parts > 1) e = launch_dq(2);
     if (e == cudaSuccess && p.parts > 1)
-        e = launch_ex(false, ckpt_dq_combine_kernel<D>, dim3((unsigned)(p.tiles * groups * 4)), dim3(256), 0, a.stream, p);
+        e = launch_ex(true, ckpt_dq_combine_kernel<D>, dim3((unsigned)(p.tiles * groups * 4)), dim3(256), 0, a.stream, p);
     if (e != cudaSuccess) return e;
     const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, a.num_sms);
     cudaLaunchConfig_t cfg = {};
@@ -916,12 +921,14 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = DkvCfg<D>::SMEM;
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, ckpt_dkdv_tc_kernel<D>, mq, mdo, mkc, mvc, mk, mv, p);
 }
 
