@@ -216,10 +216,13 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     a.n = n;
     a.dtype = c->dtype;
     a.num_sms = c->num_sms;
-    // workspace: the restored step and the statistics of its rows
-    const int pitch = std::max(n, 1);
+    // workspace: the restored step and the statistics of its rows, for C slots and the
+    // context's chunk length, so that a run of steps over a filling cache allocates once
+    CkptBwdArgs most = a;
+    most.T = std::max(T, c->tmax);
+    most.n = c->C;
     const size_t groups = (size_t)c->B * c->Hkv;
-    const size_t nq = (size_t)c->B * c->Hq * T * c->d, nk = groups * T * c->d, nK = groups * pitch * c->d;
+    const size_t nq = (size_t)c->B * c->Hq * most.T * c->d, nk = groups * most.T * c->d, nK = groups * c->C * c->d;
     size_t end = 0;
     auto take = [&](size_t b) {
         const size_t at = end;
@@ -227,10 +230,11 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
         return at;
     };
     const size_t oq = take(nq * c->elem), ok = take(nk * c->elem), ov = take(nk * c->elem);
-    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(a));
+    const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(most));
     rc = checkpoint_workspace(c, end, s);
     if (rc != H2O_OK) return rc;
     char* w = static_cast<char*>(c->ckpt_ws);
+    const int pitch = std::max(n, 1);
 
     CkptArgs r = ckpt_args(c, ckpt, T, n, s);
     r.q = w + oq;

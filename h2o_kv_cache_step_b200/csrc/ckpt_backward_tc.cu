@@ -936,8 +936,8 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
 
 size_t ckpt_stats_floats(const CkptBwdArgs& a) {
     const int groups = a.B * a.Hkv, tiles = dq_tiles(a.Hq, a.Hkv, a.T);
-    const size_t parts = dq_parts(groups, tiles, (a.n + 127) / 128 + 1, a.num_sms), table = (size_t)groups * tiles * 128;
-    return std::max((size_t)a.B * a.Hq * a.T * 4, table * 2 + (parts > 1 ? parts * table * (4 + a.d) : 0));
+    // parts exist where they and the tiles are at most num_sms
+    return std::max((size_t)a.B * a.Hq * a.T * 4, (size_t)groups * tiles * 128 * 2) + (size_t)a.num_sms * 128 * (4 + a.d);
 }
 
 cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a) {

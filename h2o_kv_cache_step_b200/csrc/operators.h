@@ -94,7 +94,8 @@ struct CkptBwdArgs {
     int num_sms;
 };
 // Floats of the workspace for the rows' statistics (and, on the tensor cores, the
-// parts of divided query tiles); needs the sizes, dtype and num_sms of a.
+// parts of divided query tiles); needs the sizes and num_sms of a, enough for any
+// smaller T and n.
 size_t ckpt_stats_floats(const CkptBwdArgs& a);
 cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a);
 cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a);  // bf16

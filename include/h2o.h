@@ -224,7 +224,8 @@ const char *h2o_last_error(const h2o_ctx *ctx);
  * see leaves the row alone whatever it holds (NaN and infinities included); a
  * row that sees a drafted node whose v holds a NaN or an infinity is NaN
  * throughout on the tensor-core path. Device pointers; layouts, element type
- * and alignment as h2o_step (parent and lse: 4 bytes). T <= H2O_TREE_MAX_T
+ * and alignment as h2o_step (parent and lse: 4 bytes); out and lse must not
+ * overlap the inputs. T <= H2O_TREE_MAX_T
  * (H2O_ERR_UNSUPPORTED otherwise, and under H2O_POLICY_INSERT_ALWAYS, where
  * the number of accepted tokens decides which slots a row may see). The scores
  * do not change: only committed tokens count. Asynchronous on `stream`. The
@@ -282,8 +283,8 @@ int h2o_checkpoint_restore(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, 
  * heads of a KV head. Rounding the record's values carries no gradient
  * (straight-through). NaNs and infinities in the record or in dout spoil the
  * gradients of their KV head. Device pointers, 16-byte aligned. The first call
- * (and one with a larger T or n) allocates a workspace; a call captured into a
- * graph needs one of its size before it. The workspace belongs to the context:
+ * (and one with T above the context's max_T and every T before) allocates a
+ * workspace; a call captured into a graph needs one of its size before it. The workspace belongs to the context:
  * its calls and replays must not overlap on the GPU. Asynchronous on `stream`. */
 int h2o_checkpoint_backward(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, int n,
                             const void *dout, void *dq, void *dK, void *dV, void *dk, void *dv,
