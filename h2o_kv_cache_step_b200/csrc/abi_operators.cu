@@ -26,6 +26,9 @@ bool capturing(cudaStream_t s) {
     return cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
 }
 
+// Counters at the start of the checkpoint workspace, one per SM, zero between calls.
+size_t ckpt_count_bytes(const h2o_ctx* c) { return (sizeof(unsigned) * c->num_sms + 255) & ~(size_t)255; }
+
 // The checkpoint workspace, at least `bytes` large.
 int checkpoint_workspace(h2o_ctx* c, size_t bytes, cudaStream_t s) {
     if (bytes <= c->ckpt_ws_bytes) return H2O_OK;
@@ -38,6 +41,12 @@ int checkpoint_workspace(h2o_ctx* c, size_t bytes, cudaStream_t s) {
     }
     void* p = nullptr;
     H2O_TRY(c, cudaMalloc(&p, bytes), "cudaMalloc(checkpoint workspace)");
+    cudaError_t e = cudaMemset(p, 0, ckpt_count_bytes(c));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        cudaFree(p);
+        return cuda_fail(c, e, "clearing the checkpoint workspace");
+    }
     if (c->ckpt_ws) c->retired.push_back(c->ckpt_ws);  // room reserved above
     c->ckpt_ws = p;
     c->ckpt_ws_bytes = bytes;
@@ -223,7 +232,7 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     most.n = c->C;
     const size_t groups = (size_t)c->B * c->Hkv;
     const size_t nq = (size_t)c->B * c->Hq * most.T * c->d, nk = groups * most.T * c->d, nK = groups * c->C * c->d;
-    size_t end = 0;
+    size_t end = ckpt_count_bytes(c);
     auto take = [&](size_t b) {
         const size_t at = end;
         end += (b + 255) & ~(size_t)255;
@@ -258,6 +267,7 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     a.dk = dk;
     a.dv = dv;
     a.stats = reinterpret_cast<float*>(w + os);
+    a.count = static_cast<unsigned*>(c->ckpt_ws);
     a.wb.err_word = c->err_dev;
     a.wb.ns = c->wait_ns;
     a.stream = s;

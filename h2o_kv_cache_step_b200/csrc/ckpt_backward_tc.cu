@@ -6,25 +6,26 @@
 // are cut into 128-row tiles whatever their heads, so that short chunks fill them;
 // the keys into 128-key blocks, the cache's and the chunk's.
 //
-// ckpt_dq_tc_kernel    one CTA per query tile, two passes over the tile's key blocks.
-//     The first computes S = Q K^T and dP = dO V^T and keeps each row's running
-//     maximum m, sum l = sum e and w = sum e dp (e = 2^(s - m)); then
-//     LSE = m + log2 l and D = w / l, in fp32. The second recomputes both products,
-//     writes dS = P (dP - D) over S in TMEM as a bf16 pair hi + lo and accumulates
-//     dQ += hi K + lo K with them as A operands from TMEM: the terms of dq cancel
-//     (sum_j ds_j = 0, and keys have much in common), so 8 bits of dS would cost
-//     it 1.7 times the rounding of the result (in 2-norm, heavy-hitter keys; dk and
-//     dv, whose terms cancel less, stay within 1.45 times with one bf16 each). The
-//     second product is 18 us of 121 at T=1024 C=2048. Where tiles are few, their blocks are divided
-//     among several CTAs: one launch for the first pass, one for the second, and
-//     ckpt_dq_combine_kernel adds up the parts in order.
-// ckpt_dkdv_tc_kernel  one CTA, or a cluster, per (KV head, 128-key block), one key
-//     per TMEM lane: per query tile of the KV head, S^T = K Q^T and dP^T = V dO^T;
-//     P^T and dS^T go back over them as bf16 and are the A operands of
-//     dV += P^T dO and dK += dS^T Q.
+// ckpt_stats_tc_kernel  one CTA per query tile: S = Q K^T and dP = dO V^T per key
+//     block, and each row's running maximum m, sum l = sum e and w = sum e dp
+//     (e = 2^(s - m)); then LSE = m + log2 l and D = w / l, in fp32.
+// ckpt_grad_tc_kernel   two kinds of CTA in one grid:
+//     dQ, one CTA per query tile: the two products again, dS = P (dP - D) over S in
+//     TMEM as a bf16 pair hi + lo, and dQ += hi K + lo K with them as A operands from
+//     TMEM: the terms of dq cancel (sum_j ds_j = 0, and keys have much in common), so
+//     8 bits of dS would cost it 1.7 times the rounding of the result (in 2-norm,
+//     heavy-hitter keys; dk and dv, whose terms cancel less, stay within 1.45 times
+//     with one bf16 each). The second product is 18 us of 121 at T=1024 C=2048.
+//     dK and dV, one CTA, or a cluster, per (KV head, 128-key block), one key per TMEM
+//     lane: per query tile of the KV head, S^T = K Q^T and dP^T = V dO^T; P^T and dS^T
+//     go back over them as bf16 and are the A operands of dV += P^T dO and
+//     dK += dS^T Q.
+// Where query tiles are few, their key blocks are divided among several CTAs: the last
+// one of a tile adds up the statistics, and ckpt_dq_combine_kernel the parts of dQ, in
+// order.
 //
-// Bound by the tensor core: 6 products of 2 d per visible (row, key) in the
-// first kernel, 4 in the second. An operand pair from shared memory needs
+// Bound by the tensor core: 2 products of 2 d per visible (row, key) for the
+// statistics, 4 for dQ and 4 for dK and dV. An operand pair from shared memory needs
 // 128 bytes a clock at the MMA's full rate, all there is, so P and dS stay in
 // TMEM (64 bytes a clock), and they never cross shared memory. Ten warps: a TMA
 // loader, an MMA issuer and two warpgroups that share every tile, one half of
@@ -64,12 +65,13 @@ struct CkptTcParams {
     int n_mblk;  // chunk key blocks = ceil(T / 128)
     int nbc;     // cache key blocks = ceil(n / 128)
     int nbC;     // 128-slot blocks of the whole cache
-    int passes;  // dQ kernel: bit 0 the first pass, bit 1 the second
-    int parts;   // dQ kernel: CTAs per query tile
+    int parts;   // CTAs per query tile, in both passes
+    int dkdv_ctas, dq_ctas;  // of the gradients' grid
     float scale_log2, scale;
     float* nL2;     // [B*Hkv][128 * tiles]: -(log2-domain LSE) per row, -inf in padding rows
     float* D;       // [B*Hkv][128 * tiles], 0 in padding rows
     float4* stat;   // parts > 1: [parts][B*Hkv][128 * tiles]: m, l, w of a part
+    unsigned* count;  // parts > 1: [B*Hkv * tiles], zero
     float4* part;   // parts > 1: [parts][B*Hkv * tiles][D / 4][128]: four columns of dQ
     __nv_bfloat16* dq;
     __nv_bfloat16* dK;
@@ -106,12 +108,11 @@ struct DqCfg {
 };
 static_assert(DqCfg<128>::SMEM_RAW <= 232448, "dQ kernel shared memory exceeds the per-CTA limit");
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-                  const __grid_constant__ CUtensorMap map_kc, const __grid_constant__ CUtensorMap map_vc,
-                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                  const CkptTcParams p) {
+// One CTA (number `cta`) of the first pass (kPass 1) or the second (kPass 2).
+template <int D, int kPass>
+__device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorMap& map_do, const CUtensorMap& map_kc,
+                                       const CUtensorMap& map_vc, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                                       const CkptTcParams& p, int cta) {
     using Cfg = DqCfg<D>;
     constexpr int RING = Cfg::RING;
     extern __shared__ uint8_t smem_raw[];
@@ -130,7 +131,7 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int part = blockIdx.x % p.parts, unit = blockIdx.x / p.parts;
+    const int part = cta % p.parts, unit = cta / p.parts;
     const int groups = p.B * p.Hkv, bg = unit % groups;
     int tile = p.tiles - 1 - unit / groups;
     if (p.T % 128 == 0)  // the heads' last tiles first: they have the most key blocks
@@ -138,7 +139,7 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     const int m0 = tile * 128;
     const int all = p.nbc + chunk_blocks(p, tile);  // key blocks: cache, then chunk
     const int jb = all * part / p.parts, nb = all * (part + 1) / p.parts - jb;  // this CTA's
-    const bool pass1 = p.passes & 1, pass2 = p.passes & 2;
+    constexpr bool pass1 = kPass == 1, pass2 = kPass == 2;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -171,7 +172,7 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         tmem = *tmem_slot;
     }
     griddep_wait();  // the kernel before has written what this one reads
-    griddep_launch_dependents();
+    if (pass1 || p.parts > 1) griddep_launch_dependents();
      // S of the two buffers at 0 and 128, dP at 256 (and 384 in pass 1), dQ at 384
     const uint32_t sbase = smem_u32(smem);
 
@@ -185,9 +186,8 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             }
             int L = 0;
             bool ok = true;
-            const int rounds = (pass1 ? nb : 0) + (pass2 ? nb : 0);
-            for (int it = 0; ok && it < rounds; ++it) {
-                const int j = jb + it % nb;
+            for (int it = 0; ok && it < nb; ++it) {
+                const int j = jb + it;
                 const bool cache = j < p.nbc;
                 const int row = 128 * (cache ? j : j - p.nbc);
                 for (int kv = 0; kv < 2; ++kv, ++L) {
@@ -242,19 +242,15 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             tc::mma_commit_warp(ring_empty + vs % RING);
         }
         // pass 2: S(t) and then dS(t) in buffer t & 1, one dP, dQ
-        for (int b = 0; b < 2 && b < n1; ++b)  // both buffers read
-            ok = ok && warp_wait(sd_free + b, ((n1 - 1 - b) >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
-        fence_after_sync();
-        const int L0 = 2 * n1;
         auto issue_s = [&](int t) {  // needs buffer t & 1 free, or read by products issued before
-            const int l = L0 + 2 * t;
+            const int l = 2 * t;
             if (!wait_ring(l)) return false;
             issue_ss(tmem + 128 * (t & 1), dQd, l % RING);
             tc::mma_commit_warp(s_full + (t & 1));
             return true;
         };
         auto issue_dp = [&](int t) {
-            const int l = L0 + 2 * t + 1;
+            const int l = 2 * t + 1;
             if (!wait_ring(l)) return false;
             issue_ss(tmem + 256, dOd, l % RING);
             tc::mma_commit_warp(dp_full);
@@ -266,7 +262,7 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             if (!(ok = warp_wait(ds_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
             if (t + 1 < n2 && !(ok = issue_dp(t + 1))) break;
-            const int ks = (L0 + 2 * t) % RING;
+            const int ks = 2 * t % RING;
             const uint64_t b = dRingN + (uint64_t)((ks * Cfg::TILE) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {  // 16 keys at a time; the keys' halves at columns 0 and 64, each hi and lo
@@ -344,52 +340,55 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             l = fmaf(l, a, l2.x + l2.y);
             w = fmaf(w, a, w2.x + w2.y);
         }
-        // the two halves of a row meet: the second hands over its m, l and w, the
-        // first gives back -LSE and D
         const bool row_ok = m0 + r < p.R;
         const size_t at = ((size_t)bg * p.tiles + tile) * 128 + r, all_rows = (size_t)groups * p.tiles * 128;
-        float nL2, Dr;
-        if (wg == 1) {
-            st[r] = m;
-            st[128 + r] = l;
-            st[256 + r] = w;
+        if (pass1) {
+            // the two halves of a row meet
+            if (wg == 1) {
+                st[r] = m;
+                st[128 + r] = l;
+                st[256 + r] = w;
+            }
             tc::named_sync(1, kConsumers);
-            tc::named_sync(2, kConsumers);
-            nL2 = st[r];
-            Dr = st[128 + r];
-        } else {
-            tc::named_sync(1, kConsumers);
-            float M = fmaxf(m, st[r]);
-            float Ms = M == -INFINITY ? 0.f : M;
-            const float a0 = ex2(m - Ms), a1 = ex2(st[r] - Ms);
-            float L = l * a0 + st[128 + r] * a1, W = w * a0 + st[256 + r] * a1;
-            if (p.parts > 1) {
-                if (pass1) {
+            if (wg == 0) {
+                float M = fmaxf(m, st[r]);
+                float Ms = M == -INFINITY ? 0.f : M;
+                const float a0 = ex2(m - Ms), a1 = ex2(st[r] - Ms);
+                float L = l * a0 + st[128 + r] * a1, W = w * a0 + st[256 + r] * a1;
+                bool mine = true;
+                if (p.parts > 1) {
+                    // the tile's last CTA adds up its parts, in order
                     p.stat[part * all_rows + at] = make_float4(M, L, W, 0.f);
-                } else {
-                    // the parts of a tile, in order
-                    M = -INFINITY;
-                    for (int q = 0; q < p.parts; ++q) M = fmaxf(M, p.stat[q * all_rows + at].x);
-                    Ms = M == -INFINITY ? 0.f : M;
-                    L = W = 0.f;
-                    for (int q = 0; q < p.parts; ++q) {
-                        const float4 x = p.stat[q * all_rows + at];
-                        const float a = ex2(x.x - Ms);
-                        L = fmaf(x.y, a, L);
-                        W = fmaf(x.z, a, W);
+                    __threadfence();
+                    tc::named_sync(2, 128);
+                    if (threadIdx.x == 64) {
+                        const bool last = atomicAdd(p.count + unit, 1u) == (unsigned)p.parts - 1;
+                        if (last) p.count[unit] = 0;
+                        st[0] = last ? 1.f : 0.f;
+                    }
+                    tc::named_sync(2, 128);
+                    mine = st[0] != 0.f;
+                    if (mine) {
+                        __threadfence();
+                        M = -INFINITY;
+                        for (int q = 0; q < p.parts; ++q) M = fmaxf(M, p.stat[q * all_rows + at].x);
+                        Ms = M == -INFINITY ? 0.f : M;
+                        L = W = 0.f;
+                        for (int q = 0; q < p.parts; ++q) {
+                            const float4 x = p.stat[q * all_rows + at];
+                            const float a = ex2(x.x - Ms);
+                            L = fmaf(x.y, a, L);
+                            W = fmaf(x.z, a, W);
+                        }
                     }
                 }
-            }
-            nL2 = -(M + log2f(L));
-            Dr = W / L;
-            st[r] = nL2;
-            st[128 + r] = Dr;
-            tc::named_sync(2, kConsumers);
-            if (pass2 && part == 0) {
-                p.nL2[at] = row_ok ? nL2 : -INFINITY;
-                p.D[at] = row_ok ? Dr : 0.f;
+                if (mine) {
+                    p.nL2[at] = row_ok ? -(M + log2f(L)) : -INFINITY;
+                    p.D[at] = row_ok ? W / L : 0.f;
+                }
             }
         }
+        const float nL2 = pass2 ? p.nL2[at] : 0.f, Dr = pass2 ? p.D[at] : 0.f;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nL2, nL2), nd2 = make_float2(-Dr, -Dr);
         for (int t = 0; pass2 && ok && t < nb; ++t) {
             const uint32_t tS = tl + 128 * (t & 1);
@@ -490,7 +489,6 @@ ckpt_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(256) ckpt_dq_combine_kernel(const CkptTcParams p) {
     griddep_wait();
-    griddep_launch_dependents();
     const int r = threadIdx.x % 32 + 32 * (blockIdx.x % 4), unit = blockIdx.x / 4;  // KV head and tile
     const int row = unit % p.tiles * 128 + r;
     if (row >= p.R) return;
@@ -527,12 +525,11 @@ struct DkvCfg {
 };
 static_assert(DkvCfg<128>::SMEM_RAW <= 232448, "dK/dV kernel shared memory exceeds the per-CTA limit");
 
+// One CTA (number `cta`), or its cluster.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-                    const __grid_constant__ CUtensorMap map_kc, const __grid_constant__ CUtensorMap map_vc,
-                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    const CkptTcParams p) {
+__device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtensorMap& map_do, const CUtensorMap& map_kc,
+                                         const CUtensorMap& map_vc, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                                         const CkptTcParams& p, int cta) {
     using Cfg = DkvCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
@@ -553,7 +550,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     // blocks in decreasing work: cache blocks (all rows see them), chunk blocks,
     // blocks of empty slots (zeros)
     const int rank = tc::cluster_rank(), ranks = tc::cluster_size();  // the cluster's CTAs share a key block
-    const int unit = blockIdx.x / ranks;
+    const int unit = cta / ranks;
     const int kb = unit / groups, bg = unit % groups;
     if (kb >= p.nbc + p.n_mblk) {
         const int s0 = 128 * (kb - p.n_mblk);
@@ -605,6 +602,7 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         tmem = *tmem_slot;
     }
     griddep_wait();  // the kernel before has written what this one reads
+    if (p.parts > 1) griddep_launch_dependents();
      // S^T at 0, dP^T at 128, dV at 256, dK at 256 + D
     const uint32_t sbase = smem_u32(smem);
 
@@ -833,21 +831,50 @@ ckpt_dkdv_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     if (ranks > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-// CTAs per key block of the dK / dV kernel. A block's query tiles are divided among
-// a cluster when there are few blocks, or when whole blocks leave SMs idle at the
-// end. The estimate, in tiles: what an SM has to do, half of a CTA's tiles as the
+// First pass: the rows' statistics.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+ckpt_stats_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                     const __grid_constant__ CUtensorMap map_kc, const __grid_constant__ CUtensorMap map_vc,
+                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const CkptTcParams p) {
+    dq_cta<D, 1>(map_q, map_do, map_kc, map_vc, map_k, map_v, p, blockIdx.x);
+}
+
+// The gradients: dK and dV by the first CTAs, dQ by the rest, in one grid, so that
+// each fills the SMs the other leaves idle (one after the other, with the first pass
+// inside dQ's kernel: 242 us a pass at T=1024 C=2048 d=128 and 55 at B=2 T=333 C=1000
+// d=64, against 202 and 52). The longer CTAs, dK and dV's, go first (the other way
+// round: 218 us).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+ckpt_grad_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                    const __grid_constant__ CUtensorMap map_kc, const __grid_constant__ CUtensorMap map_vc,
+                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    const CkptTcParams p) {
+    const int cta = blockIdx.x - p.dkdv_ctas;
+    if (cta < 0)
+        dkdv_cta<D>(map_q, map_do, map_kc, map_vc, map_k, map_v, p, blockIdx.x);
+    else if (cta < p.dq_ctas)  // the rest fills the last cluster
+        dq_cta<D, 2>(map_q, map_do, map_kc, map_vc, map_k, map_v, p, cta);
+}
+
+// CTAs per key block for dK and dV: a block's query tiles are divided among a cluster
+// when whole blocks would make a long tail. The estimate, in tiles (a query tile of a
+// key block, and a key block of a query tile, take about as long): the longest CTA if
+// all fit at once, else what an SM has to do, half of the longest CTA as the
 // unevenness of the last round, and kCtaTiles for what every CTA does besides.
-// Measured, clusters of 1, 2, 3 and 4: 110.9, 104.7, 121.7, 128.8 us at T=1024
-// C=2048 d=128 (192 blocks of up to 32 tiles), 48.3, 28.6, 22.1, 30.1 us at B=2 T=333
-// C=1000 d=64 (40 blocks of up to 24).
-int cluster_for(int groups, int tiles, int n_mblk, int nbc, int num_sms) {
-    constexpr double kCtaTiles = 5.0;
-    const double units = (double)groups * (nbc + n_mblk);
-    const double sum = (double)groups * tiles * (nbc + 0.5 * (n_mblk + 1));
+// Measured, clusters of 1, 2, 3 and 4: 202, 218, 247, 261 us a pass at T=1024 C=2048
+// d=128 (192 blocks of up to 32 tiles); 69, 53, 55, 54 at B=2 T=333 C=1000 d=64 (40
+// blocks of 21).
+int cluster_for(int groups, int tiles, int n_mblk, int nbc, int parts, int num_sms) {
+    constexpr double kCtaTiles = 6.0;
+    const double sum = 2.0 * groups * tiles * (nbc + 0.5 * (n_mblk + 1));
+    const int blocks = (nbc + n_mblk + parts - 1) / parts;
     double best = 0;
     int s_best = 1;
     for (int s = 1; s <= kMaxCluster && s <= tiles; ++s) {
-        const double ctas = units * s, most = (tiles + s - 1) / s;
+        const double ctas = (double)groups * ((nbc + n_mblk) * s + tiles * parts), most = std::max((tiles + s - 1) / s, blocks);
         const double t = ctas <= num_sms ? most + kCtaTiles : sum / num_sms + 0.5 * most + kCtaTiles * ctas / num_sms;
         if (s == 1 || t < best) {
             best = t;
@@ -869,8 +896,9 @@ int dq_parts(int groups, int tiles, int blocks, int num_sms) {
 
 template <int D>
 cudaError_t backward_launch(const CkptBwdArgs& a) {
-    if (cudaError_t e = ensure_smem_limit(ckpt_dq_tc_kernel<D>, DqCfg<D>::SMEM); e != cudaSuccess) return e;
-    if (cudaError_t e = ensure_smem_limit(ckpt_dkdv_tc_kernel<D>, DkvCfg<D>::SMEM); e != cudaSuccess) return e;
+    constexpr int kGradSmem = std::max(DqCfg<D>::SMEM, DkvCfg<D>::SMEM);
+    if (cudaError_t e = ensure_smem_limit(ckpt_stats_tc_kernel<D>, DqCfg<D>::SMEM); e != cudaSuccess) return e;
+    if (cudaError_t e = ensure_smem_limit(ckpt_grad_tc_kernel<D>, kGradSmem); e != cudaSuccess) return e;
     CUtensorMap mq, mdo, mkc, mvc, mk, mv;
     const uint64_t groups = (uint64_t)a.B * a.Hkv;
     const int R = a.Hq / a.Hkv * a.T;
@@ -905,21 +933,17 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     p.dk = static_cast<__nv_bfloat16*>(a.dk);
     p.dv = static_cast<__nv_bfloat16*>(a.dv);
     p.wb = a.wb;
-    auto launch_dq = [&](int passes) {
-        p.passes = passes;
-        return launch_ex(true, ckpt_dq_tc_kernel<D>, dim3((unsigned)(p.tiles * groups * p.parts)), dim3(kThreads),
-                         DqCfg<D>::SMEM, a.stream, mq, mdo, mkc, mvc, mk, mv, p);
-    };
-    cudaError_t e = launch_dq(p.parts > 1 ? 1 : 3);
-    if (e == cudaSuccess && p.parts > 1) e = launch_dq(2);
-    if (e == cudaSuccess && p.parts > 1)
-        e = launch_ex(true, ckpt_dq_combine_kernel<D>, dim3((unsigned)(p.tiles * groups * 4)), dim3(256), 0, a.stream, p);
+    p.count = a.count;
+    const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, p.parts, a.num_sms);
+    p.dkdv_ctas = (int)((p.nbC + p.n_mblk) * groups * ranks);
+    p.dq_ctas = (int)(p.tiles * groups * p.parts);
+    cudaError_t e = launch_ex(true, ckpt_stats_tc_kernel<D>, dim3((unsigned)p.dq_ctas), dim3(kThreads), DqCfg<D>::SMEM, a.stream,
+                              mq, mdo, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
-    const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, a.num_sms);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.nbC + p.n_mblk) * groups * ranks));
+    cfg.gridDim = dim3((unsigned)(p.dkdv_ctas + (p.dq_ctas + ranks - 1) / ranks * ranks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = DkvCfg<D>::SMEM;
+    cfg.dynamicSmemBytes = kGradSmem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -929,7 +953,9 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ckpt_dkdv_tc_kernel<D>, mq, mdo, mkc, mvc, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, ckpt_grad_tc_kernel<D>, mq, mdo, mkc, mvc, mk, mv, p);
+    if (e != cudaSuccess || p.parts == 1) return e;
+    return launch_ex(true, ckpt_dq_combine_kernel<D>, dim3((unsigned)(p.tiles * groups * 4)), dim3(256), 0, a.stream, p);
 }
 
 }  // namespace

@@ -89,6 +89,7 @@ struct CkptBwdArgs {
     void* dk;           // [B,Hkv,T,d]
     void* dv;
     float* stats;       // workspace of ckpt_stats_floats() floats
+    unsigned* count;    // num_sms words, zero between calls
     WaitBound wb;
     cudaStream_t stream;
     int num_sms;
