@@ -14,8 +14,8 @@
 //     TMEM as a bf16 pair hi + lo, and dQ += hi K + lo K with them as A operands from
 //     TMEM: the terms of dq cancel (sum_j ds_j = 0, and keys have much in common), so
 //     8 bits of dS would cost it 1.7 times the rounding of the result (in 2-norm,
-//     heavy-hitter keys; dk and dv, whose terms cancel less, stay within 1.45 times
-//     with one bf16 each). The second product is 18 us of 121 at T=1024 C=2048.
+//     heavy-hitter keys; dk and dv, whose terms cancel less, 1.4 times with one bf16
+//     each). The second product is 18 us of 121 at T=1024 C=2048.
 //     dK and dV, one CTA, or a cluster, per (KV head, 128-key block), one key per TMEM
 //     lane: per query tile of the KV head, S^T = K Q^T and dP^T = V dO^T; P^T and dS^T
 //     go back over them as bf16 and are the A operands of dV += P^T dO and
@@ -67,6 +67,7 @@ struct CkptTcParams {
     int nbC;     // 128-slot blocks of the whole cache
     int parts;   // CTAs per query tile, in both passes
     int dkdv_ctas, dq_ctas;  // of the gradients' grid
+    bool pairs;  // P and dS of dV and dK as bf16 pairs hi + lo, too
     float scale_log2, scale;
     float* nL2;     // [B*Hkv][128 * tiles]: -(log2-domain LSE) per row, -inf in padding rows
     float* D;       // [B*Hkv][128 * tiles], 0 in padding rows
@@ -85,6 +86,18 @@ struct CkptTcParams {
 __device__ __forceinline__ int chunk_blocks(const CkptTcParams& p, int tile) {
     const int r0 = 128 * tile, r1 = min(p.R, r0 + 128) - 1;
     return (r1 / p.T > r0 / p.T ? p.T - 1 : r1 % p.T) / 128 + 1;
+}
+
+// What rounding to the packed bf16 `hi` left of 64 values, as bf16, to 32 columns.
+__device__ __forceinline__ void store_rest(uint32_t taddr, const uint32_t (&x)[2][32], const uint32_t (&hi)[32]) {
+    uint32_t lo[32];
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+        const uint32_t h = hi[e >> 1];
+        lo[e >> 1] = tc::pack_bf16(__uint_as_float(x[e >> 5][e & 31]) - __uint_as_float(h << 16),
+                                   __uint_as_float(x[e >> 5][(e & 31) + 1]) - __uint_as_float(h & 0xffff0000u));
+    }
+    tc::tmem_st32(taddr, lo);
 }
 
 // ============================================================================
@@ -654,6 +667,12 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
             for (int kk = 0; kk < 8; ++kk)  // 16 rows at a time; the rows' halves at columns 0 and 64
                 tc::mma_bf16_ts_warp(acc, a + 64 * (kk >> 2) + 8 * (kk & 3), b + (uint64_t)((kk * 16 * 128) >> 4),
                                      Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
+            if (p.pairs) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_bf16_ts_warp(acc, a + 32 + 64 * (kk >> 2) + 8 * (kk & 3), b + (uint64_t)((kk * 16 * 128) >> 4),
+                                         Cfg::IDESC_G, 1u);
+            }
         };
         constexpr uint64_t kStage = (2 * Cfg::TILE) >> 4, kDO = Cfg::TILE >> 4;
         bool ok = any && warp_wait(kv_full, 0, p.wb, kDevTimeoutTmaWait, abort_flag) &&
@@ -747,6 +766,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
                 pk[(e >> 1) + 1] = tc::pack_bf16(pb.x, pb.y);
             }
             tc::tmem_st32(tl, pk);
+            if (p.pairs) store_rest(tl + 32, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -762,15 +782,16 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const float4 dr = *reinterpret_cast<const float4*>(rows + 128 + 32 * c + e);
-                    pk[16 * c + (e >> 1)] =
-                        tc::pack_bf16(__uint_as_float(s[c][e]) * (__uint_as_float(dp[e]) - dr.x),
-                                      __uint_as_float(s[c][e + 1]) * (__uint_as_float(dp[e + 1]) - dr.y));
-                    pk[16 * c + (e >> 1) + 1] =
-                        tc::pack_bf16(__uint_as_float(s[c][e + 2]) * (__uint_as_float(dp[e + 2]) - dr.z),
-                                      __uint_as_float(s[c][e + 3]) * (__uint_as_float(dp[e + 3]) - dr.w));
+                    const float d4[4] = {dr.x, dr.y, dr.z, dr.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        s[c][e + x] = __float_as_uint(__uint_as_float(s[c][e + x]) * (__uint_as_float(dp[e + x]) - d4[x]));
+                    pk[16 * c + (e >> 1)] = tc::pack_bf16(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                    pk[16 * c + (e >> 1) + 1] = tc::pack_bf16(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]));
                 }
             }
             tc::tmem_st32(tl + 128, pk);
+            if (p.pairs) store_rest(tl + 160, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -937,6 +958,14 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, p.parts, a.num_sms);
     p.dkdv_ctas = (int)((p.nbC + p.n_mblk) * groups * ranks);
     p.dq_ctas = (int)(p.tiles * groups * p.parts);
+    // dV and dK from bf16 pairs where that costs little: a small step waits for
+    // latencies, and its gradients are sums of fewer weights, whose roundings average
+    // out less (error against 64 bits, in roundings of the result: 1.2 to 1.7 with one
+    // bf16 each, 1.0 with pairs; large steps 1.4 with one). Measured, with pairs and
+    // without: 51.4 and 51.5 us a pass at B=2 T=333 C=1000 d=64 (5 products of a tile
+    // and a block per SM), 228 and 203 at T=1024 C=2048 d=128 (35 per SM).
+    constexpr int kPairWork = 16;
+    p.pairs = (long long)groups * p.tiles * (p.nbc + (p.n_mblk + 1) / 2) <= (long long)kPairWork * a.num_sms;
     cudaError_t e = launch_ex(true, ckpt_stats_tc_kernel<D>, dim3((unsigned)p.dq_ctas), dim3(kThreads), DqCfg<D>::SMEM, a.stream,
                               mq, mdo, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
