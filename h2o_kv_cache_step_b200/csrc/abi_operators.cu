@@ -10,7 +10,6 @@
 
 #include "context.h"
 #include "operators.h"
-#include "tc.h"
 
 using namespace h2o;
 

@@ -41,9 +41,9 @@
 
 #include <algorithm>
 
+#include "kernels.h"
 #include "operators.h"
-#include "tc.h"
-#include "tc_ptx.cuh"
+#include "tc_operators.cuh"
 
 namespace h2o {
 namespace {

@@ -928,20 +928,6 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_ro
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// As make_map over `outer` matrices of `rows` rows, outer_pitch rows apart: boxes
-// of box_rows rows of one matrix, rows past its end read as zeros.
-bool make_map3(CUtensorMap* m, const void* base, uint64_t rows, uint64_t outer, uint64_t outer_pitch, int d, int box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)outer};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)outer_pitch * d * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int nparts_for(int G, int T) { return (G * T + kRowsPerUnit - 1) / kRowsPerUnit; }
 
 // Pieces the cache blocks of each SDPA unit are split into: only when the
@@ -1058,10 +1044,6 @@ cudaError_t wsum_launch(const StepArgs& a) {
 
 bool tc_make_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows) {
     return make_map(m, base, rows, d, box_rows);
-}
-
-bool tc_make_map3(CUtensorMap* m, const void* base, uint64_t rows, uint64_t outer, uint64_t outer_pitch, int d, int box_rows) {
-    return make_map3(m, base, rows, outer, outer_pitch, d, box_rows);
 }
 
 bool tc_supported(int device, int d) {

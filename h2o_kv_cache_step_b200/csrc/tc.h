@@ -29,9 +29,6 @@ cudaError_t tc_wsum(const StepArgs& a);
 // 2-D TMA map over a [rows, d] bf16 matrix: boxes of box_rows rows x 64
 // columns, 128-byte swizzle (the UMMA K-major / MN-major operand layouts).
 bool tc_make_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows);
-// The same over `outer` [rows, d] matrices that start outer_pitch rows apart; a
-// box lies in one matrix, and rows past its end read as zeros.
-bool tc_make_map3(CUtensorMap* m, const void* base, uint64_t rows, uint64_t outer, uint64_t outer_pitch, int d, int box_rows);
 // Backward of the chunk SDPA on the tensor cores (bf16 inputs; fp32 gradients).
 cudaError_t tc_backward(const BwdArgs& a);
 
