@@ -5,7 +5,6 @@ current CUDA stream; every computation happens in the library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -21,16 +20,11 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_current = torch._C._cuda_getCurrentRawStream  # the current stream of a device index, as an integer
+
+
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _new_on(stream):
-    """Where a call's new tensors are made: they belong to its stream."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _record_bytes(B: int, Hq: int, Hkv: int, d: int, T: int, n: int) -> int:
@@ -184,18 +178,18 @@ class H2OCache:
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
-    def _on(self, stream, *used) -> int:
-        """The stream of a call; its inputs are marked as used there where it is
-        not the current one."""
-        current = torch._C._cuda_getCurrentRawStream(self._index)
-        if stream is None or stream.cuda_stream == current:
-            return current
+    def _on(self, stream, call, *args):
+        """call(*args) on a stream of its own: its new tensors belong to the stream,
+        its inputs are marked as used there."""
         if stream.device != self.device:
             raise ValueError(f"stream: on {stream.device}, the cache is on {self.device}")
-        for t in used:
-            if t is not None:
+        with torch.cuda.stream(stream):
+            out = call(*args)
+        for t in args:
+            t = t.buffer if isinstance(t, H2OCheckpoint) else t
+            if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
-        return stream.cuda_stream
+        return out
 
     def tree_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent: torch.Tensor, stream=None):
         """Attention of a tree of T drafted tokens per sequence over the cache,
@@ -204,34 +198,33 @@ class H2OCache:
         or any other value for an absent node. Returns (out [B,Hq,T,d], lse
         float32 [B,Hq,T]); absent rows hold 0 and -inf. Commit the accepted path
         with step()."""
+        if stream is not None:
+            return self._on(stream, self.tree_attend, q, k, v, parent)
         if q.dim() != 4:
             raise ValueError("q: need [B, Hq, T, d]")
-        B, T = self.B, q.shape[2]
+        B, T, need = self.B, q.shape[2], self._need
         chunk = (B, self.Hkv, T, self.d)
-        args = [self._need("q", q, self.dtype, (B, self.Hq, T, self.d)), self._need("k", k, self.dtype, chunk),
-                self._need("v", v, self.dtype, chunk),
-                self._need("parent", parent, torch.int32, (B, T))]
-        s = self._on(stream, q, k, v, parent)
-        with _new_on(stream):
-            out = torch.empty_like(q)
-            lse = torch.empty(B, self.Hq, T, dtype=torch.float32, device=self.device)
-        self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, s))
+        args = (need("q", q, self.dtype, (B, self.Hq, T, self.d)), need("k", k, self.dtype, chunk),
+                need("v", v, self.dtype, chunk), need("parent", parent, torch.int32, (B, T)))
+        out = torch.empty_like(q)
+        lse = torch.empty(B, self.Hq, T, dtype=torch.float32, device=self.device)
+        self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, _current(self._index)))
         return out, lse
 
     def checkpoint(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> H2OCheckpoint:
         """The inputs of the step that is about to run, in 8 bits: the chunk and
         the valid slots of the current cache."""
+        if stream is not None:
+            return self._on(stream, self.checkpoint, q, k, v)
         if q.dim() != 4:
             raise ValueError("q: need [B, Hq, T, d]")
-        B, T, n = self.B, q.shape[2], self.counters()[1]
+        B, T, n, need = self.B, q.shape[2], self.counters()[1], self._need
         chunk = (B, self.Hkv, T, self.d)
-        args = [self._need("q", q, self.dtype, (B, self.Hq, T, self.d)), self._need("k", k, self.dtype, chunk),
-                self._need("v", v, self.dtype, chunk)]
-        s = self._on(stream, q, k, v)
+        args = (need("q", q, self.dtype, (B, self.Hq, T, self.d)), need("k", k, self.dtype, chunk),
+                need("v", v, self.dtype, chunk))
         nbytes = _record_bytes(B, self.Hq, self.Hkv, self.d, T, n)
-        with _new_on(stream):
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._check(lib().h2o_checkpoint_save(self._h, *args, T, buf.data_ptr(), nbytes, s))
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._check(lib().h2o_checkpoint_save(self._h, *args, T, buf.data_ptr(), nbytes, _current(self._index)))
         return H2OCheckpoint(buf, B, self.Hq, self.Hkv, self.d, T, n)
 
     def _record(self, ck: H2OCheckpoint):
@@ -243,33 +236,31 @@ class H2OCache:
     def checkpoint_restore(self, ck: H2OCheckpoint, stream=None):
         """The values a checkpoint stands for: (q, k, v, K, V), K and V over all
         C slots with zeros in the empty ones. The cache itself is not changed."""
-        rec = self._record(ck)
-        s = self._on(stream, ck.buffer)
-        new = dict(dtype=self.dtype, device=self.device)
-        with _new_on(stream):
-            q = torch.empty(self.B, self.Hq, ck.T, self.d, **new)
-            k = torch.empty(self.B, self.Hkv, ck.T, self.d, **new)
-            K = torch.empty(self.B, self.Hkv, self.C, self.d, **new)
-            v, V = torch.empty_like(k), torch.empty_like(K)
+        if stream is not None:
+            return self._on(stream, self.checkpoint_restore, ck)
+        rec, dtype, device = self._record(ck), self.dtype, self.device
+        q = torch.empty(self.B, self.Hq, ck.T, self.d, dtype=dtype, device=device)
+        k = torch.empty(self.B, self.Hkv, ck.T, self.d, dtype=dtype, device=device)
+        K = torch.empty(self.B, self.Hkv, self.C, self.d, dtype=dtype, device=device)
+        v, V = torch.empty_like(k), torch.empty_like(K)
         self._check(lib().h2o_checkpoint_restore(self._h, *rec, q.data_ptr(), k.data_ptr(), v.data_ptr(), K.data_ptr(),
-                                                 V.data_ptr(), s))
+                                                 V.data_ptr(), _current(self._index)))
         return q, k, v, K, V
 
     def checkpoint_backward(self, ck: H2OCheckpoint, dout: torch.Tensor, stream=None):
         """Gradients of the checkpointed step's attention at the values the
         checkpoint stands for: (dq, dK, dV, dk, dv) in the cache's type, dK and
         dV over the C slots. The cache itself is not read."""
-        rec = self._record(ck)
-        do = self._need("dout", dout, self.dtype, (self.B, self.Hq, ck.T, self.d))
-        s = self._on(stream, ck.buffer, dout)
-        new = dict(dtype=self.dtype, device=self.device)
-        with _new_on(stream):
-            dq = torch.empty_like(dout)
-            dK = torch.empty(self.B, self.Hkv, self.C, self.d, **new)
-            dk = torch.empty(self.B, self.Hkv, ck.T, self.d, **new)
-            dV, dv = torch.empty_like(dK), torch.empty_like(dk)
+        if stream is not None:
+            return self._on(stream, self.checkpoint_backward, ck, dout)
+        rec, dtype, device = self._record(ck), self.dtype, self.device
+        do = self._need("dout", dout, dtype, (self.B, self.Hq, ck.T, self.d))
+        dq = torch.empty_like(dout)
+        dK = torch.empty(self.B, self.Hkv, self.C, self.d, dtype=dtype, device=device)
+        dk = torch.empty(self.B, self.Hkv, ck.T, self.d, dtype=dtype, device=device)
+        dV, dv = torch.empty_like(dK), torch.empty_like(dk)
         self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, dq.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-                                                  dk.data_ptr(), dv.data_ptr(), s))
+                                                  dk.data_ptr(), dv.data_ptr(), _current(self._index)))
         return dq, dK, dV, dk, dv
 
     def carry_grad(self, token_slots: torch.Tensor, n: int, dK: torch.Tensor, dV: torch.Tensor, dk: torch.Tensor,
@@ -281,21 +272,21 @@ class H2OCache:
         n: the valid slots before it; dK, dV, dk, dv: its own gradients. Returns
         (gK, gV, gk, gv): float32 gradients of the cache before the step, and
         the chunk's whole gradients in the cache's type."""
+        if stream is not None:
+            return self._on(stream, self.carry_grad, token_slots, n, dK, dV, dk, dv, gK_next, gV_next)
         if token_slots.dim() != 3:
             raise ValueError("token_slots: need [B, Hkv, T]")
-        T = token_slots.shape[2]
+        T, need, dtype = token_slots.shape[2], self._need, self.dtype
         cache, chunk = (self.B, self.Hkv, self.C, self.d), (self.B, self.Hkv, T, self.d)
-        slots = self._need("token_slots", token_slots, torch.int32, chunk[:3])
-        own = (self._need("dK", dK, self.dtype, cache), self._need("dV", dV, self.dtype, cache),
-               self._need("dk", dk, self.dtype, chunk), self._need("dv", dv, self.dtype, chunk))
-        later = (None if gK_next is None else self._need("gK_next", gK_next, torch.float32, cache),
-                 None if gV_next is None else self._need("gV_next", gV_next, torch.float32, cache))
-        s = self._on(stream, token_slots, dK, dV, dk, dv, gK_next, gV_next)
-        with _new_on(stream):
-            gK = torch.empty(*cache, dtype=torch.float32, device=self.device)
-            gV, gk, gv = torch.empty_like(gK), torch.empty_like(dk), torch.empty_like(dv)
+        slots = need("token_slots", token_slots, torch.int32, chunk[:3])
+        own = (need("dK", dK, dtype, cache), need("dV", dV, dtype, cache), need("dk", dk, dtype, chunk),
+               need("dv", dv, dtype, chunk))
+        later = (None if gK_next is None else need("gK_next", gK_next, torch.float32, cache),
+                 None if gV_next is None else need("gV_next", gV_next, torch.float32, cache))
+        gK = torch.empty(*cache, dtype=torch.float32, device=self.device)
+        gV, gk, gv = torch.empty_like(gK), torch.empty_like(dk), torch.empty_like(dv)
         self._check(lib().h2o_carry_grad(self._h, slots, T, int(n), *own, *later, gK.data_ptr(), gV.data_ptr(),
-                                         gk.data_ptr(), gv.data_ptr(), s))
+                                         gk.data_ptr(), gv.data_ptr(), _current(self._index)))
         return gK, gV, gk, gv
 
     def set_policy(self, policy: int) -> None:
