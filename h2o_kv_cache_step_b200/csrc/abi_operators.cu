@@ -6,7 +6,7 @@
 // that has to grow is kept until the context is destroyed, because a captured
 // graph may hold its address.
 #include <algorithm>
-#include <new>
+#include <exception>
 
 #include "context.h"
 #include "operators.h"
@@ -33,11 +33,7 @@ int checkpoint_workspace(h2o_ctx* c, size_t bytes, cudaStream_t s) {
     if (bytes <= c->ckpt_ws_bytes) return H2O_OK;
     if (capturing(s))
         return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
-    try {
-        c->retired.reserve(c->retired.size() + 1);
-    } catch (const std::bad_alloc&) {
-        return fail(c, H2O_ERR_OOM, "out of host memory");
-    }
+    c->retired.reserve(c->retired.size() + 1);
     void* p = nullptr;
     H2O_TRY(c, cudaMalloc(&p, bytes), "cudaMalloc(checkpoint workspace)");
     cudaError_t e = cudaMemset(p, 0, ckpt_count_bytes(c));
@@ -91,12 +87,16 @@ CkptArgs ckpt_args(const h2o_ctx* c, const void* ckpt, int T, int n, cudaStream_
     return a;
 }
 
+// Nothing the host code below throws (a container that finds no memory) leaves a C
+// entry.
+int thrown(h2o_ctx* c, const std::exception& e) { return fail(c, H2O_ERR_OOM, "host: %s", e.what()); }
+
 }  // namespace
 
 extern "C" {
 
 int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, const int32_t* parent, void* out,
-                    float* lse, int T, void* stream) {
+                    float* lse, int T, void* stream) try {
     int rc = check_ctx(c);
     if (rc != H2O_OK) return rc;
     if (T < 1) return fail(c, H2O_ERR_ARG, "T must be >= 1 (got %d)", T);
@@ -149,6 +149,8 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     const bool tc = c->use_tc && (long long)c->B * c->Hq * T * (c->n + T) * c->d > kTreeSimtProducts;
     H2O_TRY(c, tc ? launch_tree_tc(a) : launch_tree_simt(a), "launch tree attention");
     return H2O_OK;
+} catch (const std::exception& e) {
+    return thrown(c, e);
 }
 
 int h2o_checkpoint_bytes(const h2o_ctx* c, int T, int n, size_t* bytes) {
@@ -163,7 +165,7 @@ int h2o_checkpoint_bytes(const h2o_ctx* c, int T, int n, size_t* bytes) {
 }
 
 int h2o_checkpoint_save(h2o_ctx* c, const void* q, const void* k, const void* v, int T, void* ckpt, size_t bytes,
-                        void* stream) {
+                        void* stream) try {
     int rc = check_ctx(c);
     if (rc != H2O_OK) return rc;
     if (c->policy == H2O_POLICY_INSERT_ALWAYS)
@@ -182,10 +184,12 @@ int h2o_checkpoint_save(h2o_ctx* c, const void* q, const void* k, const void* v,
     a.V = c->Vc;
     H2O_TRY(c, launch_ckpt_save(a), "launch checkpoint save");
     return H2O_OK;
+} catch (const std::exception& e) {
+    return thrown(c, e);
 }
 
 int h2o_checkpoint_restore(h2o_ctx* c, const void* ckpt, size_t bytes, int T, int n, void* q, void* k, void* v,
-                           void* K, void* V, void* stream) {
+                           void* K, void* V, void* stream) try {
     int rc = check_ctx(c);
     if (rc == H2O_OK) rc = check_record(c, ckpt, bytes, T, n);
     if (rc != H2O_OK) return rc;
@@ -201,10 +205,12 @@ int h2o_checkpoint_restore(h2o_ctx* c, const void* ckpt, size_t bytes, int T, in
     a.V = V;
     H2O_TRY(c, launch_ckpt_restore(a), "launch checkpoint restore");
     return H2O_OK;
+} catch (const std::exception& e) {
+    return thrown(c, e);
 }
 
 int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, int n, const void* dout, void* dq,
-                            void* dK, void* dV, void* dk, void* dv, void* stream) {
+                            void* dK, void* dV, void* dk, void* dv, void* stream) try {
     int rc = check_ctx(c);
     if (rc == H2O_OK) rc = check_record(c, ckpt, bytes, T, n);
     if (rc != H2O_OK) return rc;
@@ -272,11 +278,13 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     a.stream = s;
     H2O_TRY(c, c->use_tc ? launch_ckpt_backward_tc(a) : launch_ckpt_backward_simt(a), "launch checkpoint backward");
     return H2O_OK;
+} catch (const std::exception& e) {
+    return thrown(c, e);
 }
 
 int h2o_carry_grad(h2o_ctx* c, const int32_t* token_slot, int T, int n, const void* dK, const void* dV, const void* dk,
                    const void* dv, const float* gK_next, const float* gV_next, float* gK, float* gV, void* gk, void* gv,
-                   void* stream) {
+                   void* stream) try {
     int rc = check_ctx(c);
     if (rc == H2O_OK) rc = check_chunk(c, T);
     if (rc == H2O_OK) rc = check_slots(c, n);
@@ -316,6 +324,8 @@ int h2o_carry_grad(h2o_ctx* c, const int32_t* token_slot, int T, int n, const vo
     a.stream = (cudaStream_t)stream;
     H2O_TRY(c, launch_carry(a), "launch gradient carry");
     return H2O_OK;
+} catch (const std::exception& e) {
+    return thrown(c, e);
 }
 
 }  // extern "C"

@@ -152,6 +152,20 @@ def test_tree_bad_slots_and_queries_are_not_hidden():
         assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("dtype,B", [(FP32, 1), (BF16, 1), (BF16, 16)])
+def test_tree_of_one_path_of_256_nodes(dtype, B):
+    q, k, v, K, V = heads(dtype, B, 2, 1, 64, 64, 60, 256, seed=4)
+    parent = (torch.arange(256, dtype=torch.int32, device="cuda") - 1).expand(B, 256).contiguous()
+    parent[-1, 200] = 200                  # the end of the last sequence's path is cut off
+    out, lse = cache_of(K, V, 2, 60).tree_attend(q, k, v, parent)
+    want, wlse, bound, lbound = ref.tree(q, k, v, parent, K, V, 60, dtype)
+    there = wlse > -math.inf
+    assert int((~there).sum()) == 2 * 56
+    ref.within("out", out, want, bound)
+    ref.within("lse", lse[there], wlse[there], lbound[there])
+    assert (lse[~there] == -math.inf).all() and not out[~there].any()
+
+
 @pytest.mark.parametrize("steps", [(0, 20, 21, 60, 61), (0, -90, 15, 200, 199, 500), (300, 0, -300, 310, 400)])
 @pytest.mark.parametrize("B,T", [(1, 2), (1, 70), (5, 70)])
 def test_tree_scores_that_jump_along_the_cache(steps, B, T):
@@ -312,6 +326,31 @@ def test_backward_from_a_checkpoint(dtype, B, Hkv, G, d, C, n, T):
         ref.within(name, g, w, b)
     for a, b in zip(got, c.checkpoint_backward(ck, dout)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,Hkv,G,d,n,T", [(2, 2, 3, 64, 130, 50), (1, 8, 4, 128, 2000, 500)])
+def test_backward_keeps_a_bad_kv_head_to_itself(B, Hkv, G, d, n, T):
+    """NaN and infinities in the record and in dout of one KV head (its heads, its
+    last rows and slots, next to the others' in memory) leave the rest bit for bit."""
+    q, k, v, K, V = heads(BF16, B, Hkv, G, d, n, n, T, seed=21)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(BF16)
+
+    def grads(*x):
+        c = cache_of(x[3], x[4], Hkv * G, n)
+        return c.checkpoint_backward(c.checkpoint(*x[:3]), x[5])
+
+    want = grads(q, k, v, K, V, dout)
+    b, g = B - 1, Hkv // 2
+    bad = [x.clone() for x in (q, k, v, K, V, dout)]
+    for x, h in zip(bad, (g * G + G - 1, g, g, g, g, g * G)):
+        x[b, h, -1, 3], x[b, h, 0, 5] = math.nan, math.inf
+    got = grads(*bad)
+    hit = torch.zeros((B, Hkv), dtype=torch.bool, device="cuda")
+    hit[b, g] = True
+    for name, x, y in zip(("dq", "dK", "dV", "dk", "dv"), got, want):
+        x, y = (t.view(B, Hkv, -1, d) for t in (x, y))
+        assert torch.equal(x[~hit], y[~hit]), name
+        assert x[hit].isnan().any(), name
 
 
 def test_backward_of_equal_keys():
@@ -495,6 +534,23 @@ def test_a_captured_backward_needs_its_workspace_first():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_a_captured_tree_needs_its_workspace_first(dtype):
+    q, k, v, K, V = heads(dtype, 1, 2, 2, 64, 64, 64, 8)
+    c, parent = cache_of(K, V, 4, 64), trees(1, 8)
+    with pytest.raises(H2OError, match="outside a capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            q.add_(0)  # the graph is not empty
+            c.tree_attend(q, k, v, parent)
+    want = c.tree_attend(q, k, v, parent)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = c.tree_attend(q, k, v, parent)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
 def test_refusals():
