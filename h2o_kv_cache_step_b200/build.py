@@ -1,4 +1,5 @@
-"""Build ``libh2o.so`` (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build ``libh2o.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and
+``_torch_ops.so`` (the operators' binding for torch tensors) with g++.
 
 Usage: ``python -m h2o_kv_cache_step_b200.build [--force] [--verbose]``.
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` and linked into
@@ -21,6 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libh2o.so")
+BINDING_SRC = os.path.join(CSRC, "torch_ops.cpp")
+BINDING = os.path.join(PKG, "_torch_ops.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -47,7 +50,39 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """``_torch_ops.so``, linked to the library beside it and to torch's own."""
+    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "h2o.h"), __file__))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-L", PKG, "-l:libh2o.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("build of _torch_ops.so failed")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_library(force, verbose, extra)
+    build_binding(force, verbose)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -1,7 +1,8 @@
 """``H2OCache``: one C-ABI context driven with torch tensors.
 
-Thin marshalling over ``libh2o.so``: torch provides device memory and the
-current CUDA stream; every computation happens in the library's kernels.
+Thin marshalling over ``libh2o.so`` (ctypes; ``_torch_ops.so`` for the operators
+next to the step): torch provides device memory and the current CUDA stream;
+every computation happens in the library's kernels.
 """
 from __future__ import annotations
 
@@ -20,7 +21,15 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_current = torch._C._cuda_getCurrentRawStream  # the current stream of a device index, as an integer
+def _ops_type():
+    """The operators' binding (built beside the library; no fallback exists)."""
+    lib()
+    try:
+        from . import _torch_ops
+    except ImportError as e:
+        raise ImportError(f"_torch_ops.so is missing or does not load ({e}): build it with "
+                          "`python -m h2o_kv_cache_step_b200.build`") from e
+    return _torch_ops.Ops
 
 
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
@@ -45,6 +54,13 @@ class H2OCheckpoint:
                              f"{tuple(buffer.shape)}")
         self.buffer, self.T, self.n = buffer, T, n
         self.shape = (B, Hq, Hkv, d)
+
+    @classmethod
+    def _of(cls, buffer, B, Hq, Hkv, d, T, n):
+        """A record the library has just written: of the right size."""
+        ck = cls.__new__(cls)
+        ck.buffer, ck.T, ck.n, ck.shape = buffer, T, n, (B, Hq, Hkv, d)
+        return ck
 
     @property
     def nbytes(self) -> int:
@@ -80,19 +96,22 @@ class H2OCache:
                  dtype: torch.dtype = torch.bfloat16, max_T: int | None = None):
         self.B, self.Hq, self.Hkv, self.d, self.C = B, Hq, Hkv, d, C
         self.dtype = dtype
-        self._index = torch.cuda.current_device()
-        self.device = torch.device("cuda", self._index)
+        self.device = torch.device("cuda", torch.cuda.current_device())
         h = ctypes.c_void_p()
         rc = lib().h2o_create_ex(B, Hq, Hkv, d, C, _DTYPES[dtype], int(max_T or C), ctypes.byref(h))
         check(rc, None)
         self._h = h
-        self._P, self._n = ctypes.c_int64(), ctypes.c_int64()  # what counters() reads into
+        self._ops = self._bind(h.value)
+
+    def _bind(self, handle: int):
+        return _ops_type()(handle, self.device.index, self.B, self.Hq, self.Hkv, self.d, self.C, self.dtype == torch.bfloat16)
 
     # -- lifetime -----------------------------------------------------------
     def close(self) -> None:
         if getattr(self, "_h", None):
             lib().h2o_destroy(self._h)
             self._h = None
+            self._ops = self._bind(0)  # refuses further calls
 
     def __del__(self):
         try:
@@ -170,13 +189,13 @@ class H2OCache:
         return dq, dK, dV, dk, dv
 
     # -- operators next to the step -----------------------------------------
-    # (a small call costs as much on the host as on the GPU: pointers and streams go
-    # to the library as plain integers)
-    def _need(self, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {self.device}, "
-                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
+    # (csrc/torch_ops.cpp checks the arguments, makes the outputs on the current stream
+    # and calls the library)
+    def _done(self, out):
+        """What a call returned: its outputs, or the status of one that failed."""
+        if type(out) is int:
+            self._check(out)
+        return out
 
     def _on(self, stream, call, *args):
         """call(*args) on a stream of its own: its new tensors belong to the stream,
@@ -200,52 +219,27 @@ class H2OCache:
         with step()."""
         if stream is not None:
             return self._on(stream, self.tree_attend, q, k, v, parent)
-        if q.dim() != 4:
-            raise ValueError("q: need [B, Hq, T, d]")
-        B, T, need = self.B, q.shape[2], self._need
-        chunk = (B, self.Hkv, T, self.d)
-        args = (need("q", q, self.dtype, (B, self.Hq, T, self.d)), need("k", k, self.dtype, chunk),
-                need("v", v, self.dtype, chunk), need("parent", parent, torch.int32, (B, T)))
-        out = torch.empty_like(q)
-        lse = torch.empty(B, self.Hq, T, dtype=torch.float32, device=self.device)
-        self._check(lib().h2o_tree_attend(self._h, *args, out.data_ptr(), lse.data_ptr(), T, _current(self._index)))
-        return out, lse
+        return self._done(self._ops.tree_attend(q, k, v, parent))
 
     def checkpoint(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> H2OCheckpoint:
         """The inputs of the step that is about to run, in 8 bits: the chunk and
         the valid slots of the current cache."""
         if stream is not None:
             return self._on(stream, self.checkpoint, q, k, v)
-        if q.dim() != 4:
-            raise ValueError("q: need [B, Hq, T, d]")
-        B, T, n, need = self.B, q.shape[2], self.counters()[1], self._need
-        chunk = (B, self.Hkv, T, self.d)
-        args = (need("q", q, self.dtype, (B, self.Hq, T, self.d)), need("k", k, self.dtype, chunk),
-                need("v", v, self.dtype, chunk))
-        nbytes = _record_bytes(B, self.Hq, self.Hkv, self.d, T, n)
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._check(lib().h2o_checkpoint_save(self._h, *args, T, buf.data_ptr(), nbytes, _current(self._index)))
-        return H2OCheckpoint(buf, B, self.Hq, self.Hkv, self.d, T, n)
+        buf, n = self._done(self._ops.checkpoint(q, k, v))
+        return H2OCheckpoint._of(buf, self.B, self.Hq, self.Hkv, self.d, q.shape[2], n)
 
     def _record(self, ck: H2OCheckpoint):
-        if ck.shape != (self.B, self.Hq, self.Hkv, self.d) or ck.buffer.device != self.device:
-            raise ValueError(f"checkpoint: of {ck.shape} on {ck.buffer.device}, the cache is "
-                             f"{(self.B, self.Hq, self.Hkv, self.d)} on {self.device}")
-        return ck.buffer.data_ptr(), ck.nbytes, ck.T, ck.n
+        if ck.shape != (self.B, self.Hq, self.Hkv, self.d):
+            raise ValueError(f"checkpoint: of {ck.shape}, the cache is {(self.B, self.Hq, self.Hkv, self.d)}")
+        return ck.buffer, ck.T, ck.n
 
     def checkpoint_restore(self, ck: H2OCheckpoint, stream=None):
         """The values a checkpoint stands for: (q, k, v, K, V), K and V over all
         C slots with zeros in the empty ones. The cache itself is not changed."""
         if stream is not None:
             return self._on(stream, self.checkpoint_restore, ck)
-        rec, dtype, device = self._record(ck), self.dtype, self.device
-        q = torch.empty(self.B, self.Hq, ck.T, self.d, dtype=dtype, device=device)
-        k = torch.empty(self.B, self.Hkv, ck.T, self.d, dtype=dtype, device=device)
-        K = torch.empty(self.B, self.Hkv, self.C, self.d, dtype=dtype, device=device)
-        v, V = torch.empty_like(k), torch.empty_like(K)
-        self._check(lib().h2o_checkpoint_restore(self._h, *rec, q.data_ptr(), k.data_ptr(), v.data_ptr(), K.data_ptr(),
-                                                 V.data_ptr(), _current(self._index)))
-        return q, k, v, K, V
+        return self._done(self._ops.checkpoint_restore(*self._record(ck)))
 
     def checkpoint_backward(self, ck: H2OCheckpoint, dout: torch.Tensor, stream=None):
         """Gradients of the checkpointed step's attention at the values the
@@ -253,15 +247,7 @@ class H2OCache:
         dV over the C slots. The cache itself is not read."""
         if stream is not None:
             return self._on(stream, self.checkpoint_backward, ck, dout)
-        rec, dtype, device = self._record(ck), self.dtype, self.device
-        do = self._need("dout", dout, dtype, (self.B, self.Hq, ck.T, self.d))
-        dq = torch.empty_like(dout)
-        dK = torch.empty(self.B, self.Hkv, self.C, self.d, dtype=dtype, device=device)
-        dk = torch.empty(self.B, self.Hkv, ck.T, self.d, dtype=dtype, device=device)
-        dV, dv = torch.empty_like(dK), torch.empty_like(dk)
-        self._check(lib().h2o_checkpoint_backward(self._h, *rec, do, dq.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-                                                  dk.data_ptr(), dv.data_ptr(), _current(self._index)))
-        return dq, dK, dV, dk, dv
+        return self._done(self._ops.checkpoint_backward(*self._record(ck), dout))
 
     def carry_grad(self, token_slots: torch.Tensor, n: int, dK: torch.Tensor, dV: torch.Tensor, dk: torch.Tensor,
                    dv: torch.Tensor, gK_next: torch.Tensor | None = None, gV_next: torch.Tensor | None = None,
@@ -274,20 +260,7 @@ class H2OCache:
         the chunk's whole gradients in the cache's type."""
         if stream is not None:
             return self._on(stream, self.carry_grad, token_slots, n, dK, dV, dk, dv, gK_next, gV_next)
-        if token_slots.dim() != 3:
-            raise ValueError("token_slots: need [B, Hkv, T]")
-        T, need, dtype = token_slots.shape[2], self._need, self.dtype
-        cache, chunk = (self.B, self.Hkv, self.C, self.d), (self.B, self.Hkv, T, self.d)
-        slots = need("token_slots", token_slots, torch.int32, chunk[:3])
-        own = (need("dK", dK, dtype, cache), need("dV", dV, dtype, cache), need("dk", dk, dtype, chunk),
-               need("dv", dv, dtype, chunk))
-        later = (None if gK_next is None else need("gK_next", gK_next, torch.float32, cache),
-                 None if gV_next is None else need("gV_next", gV_next, torch.float32, cache))
-        gK = torch.empty(*cache, dtype=torch.float32, device=self.device)
-        gV, gk, gv = torch.empty_like(gK), torch.empty_like(dk), torch.empty_like(dv)
-        self._check(lib().h2o_carry_grad(self._h, slots, T, int(n), *own, *later, gK.data_ptr(), gV.data_ptr(),
-                                         gk.data_ptr(), gv.data_ptr(), _current(self._index)))
-        return gK, gV, gk, gv
+        return self._done(self._ops.carry_grad(token_slots, n, dK, dV, dk, dv, gK_next, gV_next))
 
     def set_policy(self, policy: int) -> None:
         """Eviction ranking for the following steps: _lib.H2O_POLICY_SUM (the
@@ -328,8 +301,9 @@ class H2OCache:
 
     # -- inspection ---------------------------------------------------------
     def counters(self) -> tuple[int, int]:
-        self._check(lib().h2o_counters(self._h, self._P, self._n))
-        return self._P.value, self._n.value
+        P, n = ctypes.c_int64(), ctypes.c_int64()
+        self._check(lib().h2o_counters(self._h, ctypes.byref(P), ctypes.byref(n)))
+        return P.value, n.value
 
     def scores(self, stream=None) -> torch.Tensor:
         dst = torch.empty((self.B, self.Hkv, self.C), dtype=torch.float32, device=self.device)

@@ -34,15 +34,14 @@ def test_constants_match_the_header():
     assert int(re.search(r"#define H2O_CKPT_GROUP (\d+)", src).group(1)) == _lib.H2O_CKPT_GROUP
 
 
-class _Never:
-    """Stands in for a context that no refused call may reach."""
-    B, Hq, Hkv, d, C, dtype = 2, 4, 2, 64, 32, torch.bfloat16
-    device, _index = torch.device("cuda", 0), 0
-    _need = H2OCache._need
-    _record = H2OCache._record
-
-    def __getattr__(self, name):
-        raise AssertionError(f"the call went on to {name}")
+def _closed(B=2, Hq=4, Hkv=2, d=64, C=32, dtype=torch.bfloat16):
+    """A cache whose context is gone: its checks come before any call."""
+    from h2o_kv_cache_step_b200 import build
+    build.build()
+    c = H2OCache.__new__(H2OCache)
+    c.B, c.Hq, c.Hkv, c.d, c.C, c.dtype, c.device, c._h = B, Hq, Hkv, d, C, dtype, torch.device("cuda", 0), None
+    c._ops = c._bind(0)
+    return c
 
 
 def _t(*shape, dtype=torch.bfloat16):
@@ -50,28 +49,33 @@ def _t(*shape, dtype=torch.bfloat16):
 
 
 def test_host_tensors_and_wrong_shapes_are_refused():
-    c = _Never()
-    with pytest.raises(ValueError, match="q: need"):
-        H2OCache.tree_attend(c, _t(2, 4, 5), _t(2, 2, 5, 64), _t(2, 2, 5, 64), _t(2, 5, dtype=torch.int32))
-    with pytest.raises(ValueError, match="q: need a contiguous"):
-        H2OCache.tree_attend(c, _t(2, 4, 5, 64), _t(2, 2, 5, 64), _t(2, 2, 5, 64), _t(2, 5, dtype=torch.int32))
-    with pytest.raises(ValueError, match="token_slots: need"):
-        H2OCache.carry_grad(c, _t(2, 5, dtype=torch.int32), 3, *[_t(2, 2, 5, 64)] * 4)
-    with pytest.raises(ValueError, match="token_slots: need a contiguous"):
-        H2OCache.carry_grad(c, _t(2, 2, 5, dtype=torch.int32), 3, *[_t(2, 2, 5, 64)] * 4)
+    c = _closed()
+    tree = _t(2, 5, dtype=torch.int32)
+    with pytest.raises(ValueError, match=r"q: need \[B, Hq, T, d\]"):
+        c.tree_attend(_t(2, 4, 5), _t(2, 2, 5, 64), _t(2, 2, 5, 64), tree)
+    with pytest.raises(ValueError, match="q: need a contiguous BFloat16 tensor of shape .2, 4, 5, 64. on cuda:0, got BFloat16 .* on cpu"):
+        c.tree_attend(_t(2, 4, 5, 64), _t(2, 2, 5, 64), _t(2, 2, 5, 64), tree)
+    with pytest.raises(TypeError, match="q: need a tensor"):
+        c.checkpoint(None, _t(2, 2, 5, 64), _t(2, 2, 5, 64))
+    with pytest.raises(ValueError, match=r"token_slots: need \[B, Hkv, T\]"):
+        c.carry_grad(tree, 3, *[_t(2, 2, 5, 64)] * 4)
+    with pytest.raises(ValueError, match="token_slots: need a contiguous Int"):
+        c.carry_grad(_t(2, 2, 5, dtype=torch.int32), 3, *[_t(2, 2, 5, 64)] * 4)
+    with pytest.raises(TypeError):
+        c.carry_grad(_t(2, 2, 5, dtype=torch.int32), 3.5, *[_t(2, 2, 5, 64)] * 4)
+    with pytest.raises(ValueError, match="n: out of range"):
+        c.carry_grad(_t(2, 2, 5, dtype=torch.int32), 1 << 40, *[_t(2, 2, 5, 64)] * 4)
 
 
 def test_a_record_of_another_size_or_place_is_refused():
     rows = 2 * (4 * 5 + 2 * 2 * 5 + 2 * 2 * 3)
     with pytest.raises(ValueError, match="buffer: need"):
         H2OCheckpoint(torch.zeros(rows * (64 + 8), dtype=torch.uint8), 2, 4, 2, 64, 5, 3)
-    ck = H2OCheckpoint.__new__(H2OCheckpoint)
-    ck.buffer, ck.shape, ck.T, ck.n = torch.zeros(rows * 72, dtype=torch.uint8), (2, 4, 2, 64), 5, 3
+    ck = H2OCheckpoint._of(torch.zeros(rows * 72, dtype=torch.uint8), 2, 4, 2, 64, 5, 3)
+    with pytest.raises(ValueError, match="checkpoint: need a contiguous Byte"):
+        _closed().checkpoint_restore(ck)
     with pytest.raises(ValueError, match="checkpoint: of"):
-        H2OCache._record(_Never(), ck)
-    ck.shape = (2, 4, 4, 64)
-    with pytest.raises(ValueError, match="checkpoint: of"):
-        H2OCache._record(_Never(), ck)
+        _closed(Hkv=4).checkpoint_restore(ck)
 
 
 def test_a_record_splits_into_its_sections():
