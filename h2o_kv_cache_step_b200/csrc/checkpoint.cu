@@ -28,6 +28,7 @@
 // once (43.1 us; twice 46.3).
 #include <math.h>
 
+#include "kernels.h"
 #include "operators.h"
 #include "vec.cuh"
 
@@ -156,6 +157,8 @@ ckpt_save_kernel(const __grid_constant__ Sections sec, int8_t* __restrict__ code
     constexpr int kIter = kSaveIter;
     const Place p = place<D, kIter>(sec);
     const E* src = static_cast<const E*>(p.x) + p.row * D + p.col;
+    griddep_wait();  // the work before is complete; what follows may set up
+    griddep_launch_dependents();
     float all[kIter][kPer] = {};
 #pragma unroll
     for (int it = 0; it < kIter; ++it)
@@ -188,9 +191,10 @@ ckpt_save_kernel(const __grid_constant__ Sections sec, int8_t* __restrict__ code
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads)
 ckpt_restore_kernel(const __grid_constant__ Sections sec, const int8_t* __restrict__ codes, const float* __restrict__ scales) {
-    griddep_launch_dependents();  // the backward's first kernel waits for this grid's end before it reads
     constexpr int kIter = kRestoreIter;
     const Place p = place<D, kIter>(sec);
+    griddep_wait();  // the work before is complete; what follows may set up
+    griddep_launch_dependents();
     if (p.x == nullptr) return;
     E* dst = static_cast<E*>(p.x) + p.row * D + p.col;
     uint4 w[kIter];
@@ -244,15 +248,14 @@ Sections sections(const CkptArgs& a, bool restore) {
 template <typename E, int D>
 cudaError_t save_typed(const CkptArgs& a) {
     const Sections sec = sections(a, false);
-    ckpt_save_kernel<E, D><<<sec.s[4].block_end, kThreads, 0, a.stream>>>(sec, a.codes, a.scales);
-    return cudaGetLastError();
+    return launch_ex(true, ckpt_save_kernel<E, D>, dim3(sec.s[4].block_end), dim3(kThreads), 0, a.stream, sec, a.codes, a.scales);
 }
 
 template <typename E, int D>
 cudaError_t restore_typed(const CkptArgs& a) {
     const Sections sec = sections(a, true);
-    ckpt_restore_kernel<E, D><<<sec.s[4].block_end, kThreads, 0, a.stream>>>(sec, a.codes, a.scales);
-    return cudaGetLastError();
+    return launch_ex(true, ckpt_restore_kernel<E, D>, dim3(sec.s[4].block_end), dim3(kThreads), 0, a.stream, sec,
+                     (const int8_t*)a.codes, (const float*)a.scales);
 }
 
 // ============================================================================
@@ -278,6 +281,8 @@ carry_kernel(const int32_t* __restrict__ token_slot, const E* __restrict__ dK, c
     const int blk = blockIdx.x % per;
     const int32_t* slots = token_slot + bg * T;
     constexpr int PER_ROW = D / 4;
+    griddep_wait();  // the work before is complete; what follows may set up
+    griddep_launch_dependents();
     if (blk < slot_blocks) {
         const int s0 = blk * kCarryRows;
         if (threadIdx.x < kCarryRows) taken[threadIdx.x] = 0;
@@ -324,10 +329,10 @@ carry_kernel(const int32_t* __restrict__ token_slot, const E* __restrict__ dK, c
 template <typename E, int D>
 cudaError_t carry_typed(const CarryArgs& a) {
     const int sb = (a.C + kCarryRows - 1) / kCarryRows, tb = (a.T + kCarryRows - 1) / kCarryRows;
-    carry_kernel<E, D><<<(unsigned)(a.B * a.Hkv * (sb + tb)), kThreads, 0, a.stream>>>(
+    return launch_ex(
+        true, carry_kernel<E, D>, dim3((unsigned)(a.B * a.Hkv * (sb + tb))), dim3(kThreads), 0, a.stream,
         a.token_slot, (const E*)a.dK, (const E*)a.dV, (const E*)a.dk, (const E*)a.dv, a.gK_next, a.gV_next, a.gK, a.gV,
         (E*)a.gk, (E*)a.gv, a.C, a.T, a.n, sb, tb);
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 
+#include "kernels.h"
 #include "operators.h"
 #include "vec.cuh"
 
@@ -60,6 +61,8 @@ tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __re
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane >> 3, l8 = lane & 7;
     const size_t row0 = (size_t)bg * R + r0;  // [B,Hq,T] rows of a group are contiguous
 
+    griddep_wait();  // the work before is complete; what follows may set up
+    griddep_launch_dependents();
     // the path of each row's node to the root: parents have smaller indices, so
     // the walk ends
     if (hi > n) {
@@ -246,10 +249,9 @@ cudaError_t tree_simt_rows(const TreeArgs& a) {
     s.o = a.part;
     s.ml = reinterpret_cast<float2*>(a.part + (size_t)a.num_sms * kRows * D);
     s.count = a.count;
-    tree_simt_kernel<E, D, kRows><<<(unsigned)(units * s.parts), kWarps * 32, 0, a.stream>>>(
-        (const E*)a.q, (const E*)a.k, (const E*)a.v, a.parent, (const E*)a.Kc, (const E*)a.Vc, (E*)a.out, a.lse, a.Hq,
-        a.Hkv, a.C, a.T, a.n, per, kLog2e / sqrtf((float)D), s);
-    return cudaGetLastError();
+    return launch_ex(true, tree_simt_kernel<E, D, kRows>, dim3((unsigned)(units * s.parts)), dim3(kWarps * 32), 0, a.stream,
+                     (const E*)a.q, (const E*)a.k, (const E*)a.v, a.parent, (const E*)a.Kc, (const E*)a.Vc, (E*)a.out, a.lse,
+                     a.Hq, a.Hkv, a.C, a.T, a.n, per, kLog2e / sqrtf((float)D), s);
 }
 
 // Four rows a CTA while that gives every SM a CTA, by rows or by slices of the keys.

@@ -235,7 +235,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tmem = *tmem_slot;
     }
     const uint32_t sbase = smem_u32(smem);
-    griddep_launch_dependents();  // the merge waits for this grid's end before it reads
+    griddep_wait();  // the work before is complete; what follows may set up
+    griddep_launch_dependents();
 
     if (warp == 0) {
         // ------------------------------------------------------------ loader
@@ -647,6 +648,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
 tree_combine_kernel(const TreeParams p, unsigned rows) {
     griddep_wait();
+    griddep_launch_dependents();
     constexpr unsigned kRows = 1024 / D;
     const unsigned g = blockIdx.x * kRows + threadIdx.x % kRows;
     if (g < rows) merge_row<D>(p, g / (unsigned)p.R, (int)(g % (unsigned)p.R), threadIdx.x / kRows);
@@ -699,7 +701,7 @@ cudaError_t tree_launch(const TreeArgs& a) {
     // one token over 2048 slots, 14.4 us a pass against 15.4 with a kernel.
     constexpr int kMergeRows = 32;
     p.count = by_unit && R <= kMergeRows ? a.count : nullptr;
-    cudaError_t e = launch_ex(false, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
+    cudaError_t e = launch_ex(true, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
     bool divided = false;
     for (int c = 1; c < ctas && !divided; ++c) divided = p.split.first(c) % p.nb != 0;
