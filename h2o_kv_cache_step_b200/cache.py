@@ -190,7 +190,8 @@ class H2OCache:
 
     # -- operators next to the step -----------------------------------------
     # (csrc/torch_ops.cpp checks the arguments, makes the outputs on the current stream
-    # and calls the library)
+    # and calls the library). Like the steps, the calls of a cache and replays of graphs
+    # that hold some follow one another on the GPU: they share its workspaces.
     def _done(self, out):
         """What a call returned: its outputs, or the status of one that failed."""
         if type(out) is int:

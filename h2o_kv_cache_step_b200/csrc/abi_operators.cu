@@ -116,9 +116,15 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
             return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
         const size_t words = std::max((size_t)c->B * c->Hkv, (size_t)c->num_sms);
         if (!c->tree_count) {
-            H2O_TRY(c, cudaMalloc(&c->tree_count, sizeof(unsigned) * words), "cudaMalloc(tree workspace)");
-            H2O_TRY(c, cudaMemset(c->tree_count, 0, sizeof(unsigned) * words), "cudaMemset(tree workspace)");
-            H2O_TRY(c, cudaStreamSynchronize(nullptr), "cudaMemset(tree workspace)");
+            unsigned* count = nullptr;
+            H2O_TRY(c, cudaMalloc(&count, sizeof(unsigned) * words), "cudaMalloc(tree workspace)");
+            cudaError_t e = cudaMemset(count, 0, sizeof(unsigned) * words);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+            if (e != cudaSuccess) {
+                cudaFree(count);
+                return cuda_fail(c, e, "clearing the tree workspace");
+            }
+            c->tree_count = count;
         }
         const size_t floats = c->use_tc ? tree_part_floats(c->num_sms, c->d) : tree_simt_part_floats(c->num_sms, c->d);
         H2O_TRY(c, cudaMalloc(&c->tree_part, sizeof(float) * floats), "cudaMalloc(tree workspace)");

@@ -393,6 +393,62 @@ def test_carry(dtype, B, Hkv, d, C, n, T, last):
         ref.within("chunk", tok, chunk, (ref.U[dtype] + 2 * ref.U32) * chunk.abs())
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_offsets_past_32_bits(dtype):
+    """K and V of 2^31 values and more, looked at where they end: the last KV head
+    of the last sequence, its rows drawn to slots near the cache's end."""
+    B, Hkv, d, T, C = 2, 8, 128, 2, 2**20 + 77
+    q, k, v, Ke, Ve = heads(dtype, 1, 1, 1, d, C, C, T, seed=5)
+    for t in range(T):
+        Ke[0, 0, C - 1 - 99 * t] = (20 * q[0, 0, t].float() / q[0, 0, t].float().norm()).to(dtype)
+
+    def last(x, fill=0):  # x as the last head of them all
+        whole = torch.full((B, Hkv, *x.shape[2:]), fill, dtype=x.dtype, device="cuda")
+        whole[-1, -1] = x[0, 0]
+        return whole
+
+    def end(x):
+        return x[-1:, -1:].clone()
+
+    c = cache_of(last(Ke), last(Ve), Hkv, C, max_T=8)
+    torch.cuda.empty_cache()
+    whole = [last(x) for x in (q, k, v)]
+    parent = torch.tensor([[-1, -2], [-1, 0]], dtype=torch.int32, device="cuda")
+    out, lse = c.tree_attend(*whole, parent)
+    c.sync_check()
+    want, wlse, bound, lbound = ref.tree(q, k, v, parent[1:], Ke, Ve, C, dtype)
+    ref.within("out", end(out), want, bound)
+    ref.within("lse", end(lse), wlse, lbound)
+
+    ck = c.checkpoint(*whole)
+    rest = c.checkpoint_restore(ck)
+    c.sync_check()
+    for x, got in zip((q, k, v, Ke, Ve), rest):
+        assert torch.equal(ref.quantise(x)[2], end(got)) and not got[0, 0].any()
+    rest = [end(x) for x in rest]
+    torch.cuda.empty_cache()
+
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(dtype)
+    got = c.checkpoint_backward(ck, last(dout))
+    c.sync_check()
+    want, bound = ref.backward(*rest, dout, C, dtype)
+    for name, g, w, b in zip(("dq", "dK", "dV", "dk", "dv"), got, want, bound):
+        assert not g[0, 0].any()
+        ref.within(name, end(g), w, b)
+    del ck, want, bound, rest
+    torch.cuda.empty_cache()
+
+    slots = torch.tensor([[[-1, C - 3]]], dtype=torch.int32, device="cuda")
+    nxt = torch.randn(Ke.shape, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    gnext = last(nxt)
+    gK, gV, gk, gv = c.carry_grad(last(slots, fill=-1), C, *got[1:], gnext, gnext)
+    c.sync_check()
+    for g, tok, own, ch in ((gK, gk, got[1], got[3]), (gV, gv, got[2], got[4])):
+        before, chunk = ref.carry(slots, C, end(own), end(ch), nxt)
+        ref.within("cache", end(g), before, ref.U32 * before.abs())
+        ref.within("chunk", end(tok), chunk, (ref.U[dtype] + 2 * ref.U32) * chunk.abs())
+
+
 # ---- together -----------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [FP32, BF16])
 def test_training_run(dtype):
