@@ -41,13 +41,64 @@ struct TreeSplit {
     unsigned* count;  // [rows / kRows], zero
 };
 
+// A key's or a query's channels as eight lanes hold them, 16 bytes at a time: value i
+// of lane l8 is channel 8 kVec (i / kVec) + kVec l8 + i % kVec.
+template <typename E>
+constexpr int kVec = 16 / (int)sizeof(E);
+
+template <typename E, int N>
+__device__ __forceinline__ void load_lane(const E* row, int l8, uint4 (&w)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) w[c] = *reinterpret_cast<const uint4*>(row + 8 * kVec<E> * c + kVec<E> * l8);
+}
+template <int N>
+__device__ __forceinline__ void expand(const uint4 (&w)[N], float (&f)[4 * N], float) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        f[4 * c] = __uint_as_float(w[c].x);
+        f[4 * c + 1] = __uint_as_float(w[c].y);
+        f[4 * c + 2] = __uint_as_float(w[c].z);
+        f[4 * c + 3] = __uint_as_float(w[c].w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void expand(const uint4 (&w)[N], float (&f)[8 * N], __nv_bfloat16) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[8 * c + 2 * j] = __uint_as_float(u[j] << 16);
+            f[8 * c + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+    }
+}
+// The channel of the first of four values: values 4 j .. 4 j + 3 of lane l8 are
+// kept at 4 (8 j + l8) of a row in shared memory (no two lanes in a bank) and of
+// the parts; `four` counts those.
+template <typename E>
+__device__ __forceinline__ int channel(int four) {
+    const int i = 4 * (four >> 3), l8 = four & 7;
+    return 8 * kVec<E> * (i / kVec<E>) + kVec<E> * l8 + i % kVec<E>;
+}
+
+// Adds one; what the CTA wrote before its barrier is visible to whoever counts after.
+__device__ __forceinline__ unsigned count_acq_rel(unsigned* count) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
+    return old;
+}
+
 template <typename E, int D, int kRows>
 __global__ void __launch_bounds__(kWarps * 32)
 tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
                  const int32_t* __restrict__ parent, const E* __restrict__ Kc, const E* __restrict__ Vc,
                  E* __restrict__ out, float* __restrict__ lse, int Hq, int Hkv, int C, int T, int n, int blocks_per_group,
                  float scale_log2, const TreeSplit split) {
-    constexpr int Q4 = D / 32;  // float4 per lane and row
+    constexpr int kLane = D / 8;                         // values per lane and row
+    constexpr int kLoads = kLane / kVec<E>;              // 16-byte loads of them
+    constexpr int kBatch = sizeof(E) == 4 && kRows == 4 ? 2 : 4;  // keys in flight per lane group
+    constexpr int kStride = kWarps * 4;                  // keys of the CTA at a time
     __shared__ int up[kTreeMaxT];
     __shared__ int last;
     __shared__ uint32_t mask[kRows][kTreeMaskWords];
@@ -63,11 +114,36 @@ tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __re
 
     griddep_wait();  // the work before is complete; what follows may set up
     griddep_launch_dependents();
+    uint4 kw[kBatch][kLoads], vw[kBatch][kLoads];
+    // the keys u0 + kStride b + sub; past the slice its last one, not used
+    auto load = [&](int u0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = min(u0 + kStride * b + sub, hi - 1);
+            const size_t at = u < n ? ((size_t)bg * C + u) * D : ((size_t)bg * T + (u - n)) * D;
+            load_lane((u < n ? Kc : k) + at, l8, kw[b]);
+            load_lane((u < n ? Vc : v) + at, l8, vw[b]);
+        }
+    };
+    int u0 = lo + warp * 4;
+    if (u0 < hi) load(u0);
     // the path of each row's node to the root: parents have smaller indices, so
     // the walk ends
     if (hi > n) {
         for (int i = threadIdx.x; i < T; i += kWarps * 32) up[i] = parent[(size_t)(bg / Hkv) * T + i];
         __syncthreads();
+    }
+    float qf[kRows][kLane], acc[kRows][kLane];
+    float m[kRows], l[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        uint4 w[kLoads];
+        load_lane(q + (row0 + min(r, R - 1 - r0)) * D, l8, w);
+        expand(w, qf[r], E());
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) acc[r][i] = 0.f;
     }
     if (threadIdx.x < kRows) {
         const int r = threadIdx.x;
@@ -80,61 +156,68 @@ tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __re
         }
         present[r] = at == -1;
     }
-    float4 qr[kRows][Q4], acc[kRows][Q4];
-    float m[kRows], l[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-        const size_t row = row0 + min(r, R - 1 - r0);
-#pragma unroll
-        for (int c = 0; c < Q4; ++c) {
-            qr[r][c] = load4(q + row * D + 32 * c + 4 * l8);
-            acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    }
     __syncthreads();
 
-#pragma unroll 2
-    for (int u0 = lo + warp * 4; u0 < hi; u0 += kWarps * 4) {
-        const int u = u0 + sub;
-        const bool in = u < hi;
-        const int uu = in ? u : hi - 1;
-        const E* kp = uu < n ? Kc + ((size_t)bg * C + uu) * D : k + ((size_t)bg * T + (uu - n)) * D;
-        const E* vp = uu < n ? Vc + ((size_t)bg * C + uu) * D : v + ((size_t)bg * T + (uu - n)) * D;
-        float4 kk[Q4], vv[Q4];
+    while (u0 < hi) {
+        float s[kRows][kBatch];
+        uint32_t vis[kBatch];  // rows that see the key
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) kk[c] = load4(kp + 32 * c + 4 * l8);
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = u0 + kStride * b + sub;
+            float kf[kLane];
+            expand(kw[b], kf, E());
+            vis[b] = 0;
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) vv[c] = load4(vp + 32 * c + 4 * l8);
+            for (int r = 0; r < kRows; ++r) {
+                float x = 0.f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float s = 0.f;
-#pragma unroll
-            for (int c = 0; c < Q4; ++c)
-                s = fmaf(qr[r][c].x, kk[c].x, fmaf(qr[r][c].y, kk[c].y, fmaf(qr[r][c].z, kk[c].z, fmaf(qr[r][c].w, kk[c].w, s))));
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            // a key the row does not see touches nothing, whatever it holds
-            const bool vis = in && (u < n || ((mask[r][(u - n) >> 5] >> ((u - n) & 31)) & 1u));
-            s *= scale_log2;
-            const float mn = fmaxf(m[r], s);
-            if (vis && !(s == mn && mn == -INFINITY)) {
-                const float a = exp2f(m[r] - mn), p = exp2f(s - mn);
-                l[r] = fmaf(l[r], a, p);
-                m[r] = mn;
-#pragma unroll
-                for (int c = 0; c < Q4; ++c) {
-                    acc[r][c].x = fmaf(p, vv[c].x, acc[r][c].x * a);
-                    acc[r][c].y = fmaf(p, vv[c].y, acc[r][c].y * a);
-                    acc[r][c].z = fmaf(p, vv[c].z, acc[r][c].z * a);
-                    acc[r][c].w = fmaf(p, vv[c].w, acc[r][c].w * a);
-                }
+                for (int i = 0; i < kLane; ++i) x = fmaf(qf[r][i], kf[i], x);
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                const bool see = u < hi && (u < n || ((mask[r][(u - n) >> 5] >> ((u - n) & 31)) & 1u));
+                vis[b] |= (uint32_t)see << r;
+                s[r][b] = see ? x * scale_log2 : -INFINITY;
             }
         }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float mn = m[r];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) mn = fmaxf(mn, s[r][b]);
+            const float ms = mn == -INFINITY ? 0.f : mn, a = exp2f(m[r] - ms);
+            m[r] = mn;
+            l[r] *= a;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                s[r][b] = exp2f(s[r][b] - ms);
+                l[r] += s[r][b];
+            }
+#pragma unroll
+            for (int i = 0; i < kLane; ++i) acc[r][i] *= a;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            float vf[kLane];
+            expand(vw[b], vf, E());
+            if (vis[b] == (1u << kRows) - 1) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int i = 0; i < kLane; ++i) acc[r][i] = fmaf(s[r][b], vf[i], acc[r][i]);
+            } else {  // a key the row does not see touches nothing, whatever it holds
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (vis[b] >> r & 1u)
+#pragma unroll
+                        for (int i = 0; i < kLane; ++i) acc[r][i] = fmaf(s[r][b], vf[i], acc[r][i]);
+            }
+        }
+        u0 += kStride * kBatch;
+        if (u0 < hi) load(u0);
     }
-    // merge the four lane groups of a warp, then the warps
+    // merge the four lane groups of a warp: each ends with a quarter of the rows' values
+    float x[kRows * kLane];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         float M = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8));
@@ -144,54 +227,71 @@ tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __re
         L += __shfl_xor_sync(0xffffffffu, L, 8);
         L += __shfl_xor_sync(0xffffffffu, L, 16);
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) {
-            float x[4] = {acc[r][c].x * w, acc[r][c].y * w, acc[r][c].z * w, acc[r][c].w * w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] += __shfl_xor_sync(0xffffffffu, x[e], 8);
-                x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
-            }
-            if (sub == 0) *reinterpret_cast<float4*>(&part[warp][r][32 * c + 4 * l8]) = make_float4(x[0], x[1], x[2], x[3]);
-        }
+        for (int i = 0; i < kLane; ++i) x[r * kLane + i] = acc[r][i] * w;
         if (lane == 0) {
             part_m[warp][r] = M;
             part_l[warp][r] = L;
         }
     }
+    constexpr int kHalf = kRows * kLane / 2, kQuarter = kHalf / 2;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+        const float send = sub & 2 ? x[i] : x[kHalf + i], keep = sub & 2 ? x[kHalf + i] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kQuarter; ++i) {
+        const float send = sub & 1 ? x[i] : x[kQuarter + i], keep = sub & 1 ? x[kQuarter + i] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
+    }
+    {
+        const int r = kRows == 1 ? 0 : sub, i0 = kRows == 1 ? sub * kQuarter : 0;  // value 0 of the quarter
+        static_assert(kRows == 1 || kRows == 4, "a quarter is a row or a part of the only one");
+        float* dst = &part[warp][r][32 * (i0 / 4) + 4 * l8 + i0 % 4];
+        if constexpr (kQuarter == 2) {
+            *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kQuarter / 4; ++j)
+                *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        }
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < kRows * D; e += kWarps * 32) {
-        const int r = e / D, x = e % D;
-        if (r0 + r >= R) continue;
-        float M = -INFINITY, L = 0.f, o = 0.f;
+    // merge the warps, four values per thread
+    constexpr int kItems = kRows * (D / 4);
+    const int item = threadIdx.x % kItems, g = threadIdx.x / kItems, r = item / (D / 4), c4 = item % (D / 4);
+    if (g == 0 && r0 + r < R) {
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_m[w][r]);
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = part_m[w][r] == -INFINITY && part_l[w][r] == 0.f ? 0.f : exp2f(part_m[w][r] - M);
             L = fmaf(part_l[w][r], f, L);
-            o = fmaf(part[w][r][x], f, o);
+            o = fma4(f, load4(&part[w][r][4 * c4]), o);
         }
         if (split.parts > 1) {
             const size_t at = ((size_t)unit * split.parts + piece) * kRows + r;
-            split.o[at * D + x] = o;
-            if (x == 0) split.ml[at] = make_float2(present[r] ? M : __uint_as_float(0x7fffffffu), L);
+            store4(split.o + at * D + 4 * c4, o);
+            if (c4 == 0) split.ml[at] = make_float2(present[r] ? M : __uint_as_float(0x7fffffffu), L);
         } else {
-            out[(row0 + r) * D + x] = from_f32<E>(present[r] ? o / L : 0.f);
-            if (x == 0) lse[row0 + r] = present[r] ? (M + log2f(L)) * kLn2 : -INFINITY;
+            store4(out + (row0 + r) * D + channel<E>(c4),
+                   present[r] ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L) : make_float4(0.f, 0.f, 0.f, 0.f));
+            if (c4 == 0) lse[row0 + r] = present[r] ? (M + log2f(L)) * kLn2 : -INFINITY;
         }
     }
     if (split.parts == 1) return;
-    __threadfence();
-    __syncthreads();
+    __syncthreads();  // the CTA's part is written, and released with the count
     if (threadIdx.x == 0) {
-        last = atomicAdd(split.count + unit, 1u) == (unsigned)split.parts - 1;
+        last = count_acq_rel(split.count + unit) == (unsigned)split.parts - 1;
         if (last) split.count[unit] = 0;
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     // kGroups threads share four columns of a row, every kGroups-th part each, and meet
     // in shared memory
-    constexpr int kItems = kRows * (D / 4), kGroups = kItems * kWarps <= kWarps * 32 ? kWarps : kWarps * 32 / kItems;
-    const int item = threadIdx.x % kItems, g = threadIdx.x / kItems, r = item / (D / 4), c4 = item % (D / 4);
+    constexpr int kGroups = kItems * kWarps <= kWarps * 32 ? kWarps : kWarps * 32 / kItems;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     bool absent = false;
@@ -234,7 +334,7 @@ tree_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __re
         L = fmaf(part_l[p][r], w, L);
         o = fma4(w, load4(&part[p][r][4 * c4]), o);
     }
-    store4(out + (row0 + r) * D + 4 * c4, absent ? make_float4(0.f, 0.f, 0.f, 0.f) : scale4(o, 1.f / L));
+    store4(out + (row0 + r) * D + channel<E>(c4), absent ? make_float4(0.f, 0.f, 0.f, 0.f) : scale4(o, 1.f / L));
     if (c4 == 0) lse[row0 + r] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
