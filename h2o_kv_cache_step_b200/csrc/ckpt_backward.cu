@@ -19,10 +19,13 @@
 namespace h2o {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kStride = kWarps * 4;  // keys or rows of a CTA at a time
 // dq: query rows per CTA, and dk, dv: keys per CTA, in registers: two where that still
 // gives every SM two CTAs, one otherwise (64 rows, 320 keys, 4 / 2 heads: dq 9.6 us with
-// two and 8.0 with one, dk and dv 6.3 and 8.1).
+// two and 8.0 with one, dk and dv 6.3 and 8.1). A lane group then has two or four keys
+// (rows) in flight: bound by the latency of its loads in small steps, by the fp32
+// pipe in large ones (one at a time, and so: 15.4 and 14.2 us a pass at 64 rows, 256
+// slots, 4 / 2 heads, d = 64; 2748 and 2120 at 256 rows, 2048 slots, 32 / 8 heads, d = 128).
 
 __device__ __forceinline__ float sum8(float x) {  // over the eight lanes of a key or row
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -42,13 +45,14 @@ __device__ __forceinline__ float4 sum_subs(float4 a) {
 // A = sum e dp k, Z = sum e k, sum e dp and sum e (e = exp(s - max)):
 // dq = (A - D Z) / (sum e sqrt(d)). Eight lanes share a key.
 template <typename E, int D, int kRows>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kRows * D <= 128 ? 2 : 1)
 ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
                     const E* __restrict__ V, const E* __restrict__ dout, E* __restrict__ dq, float4* __restrict__ stats,
                     int G, int T, int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
     griddep_wait();  // the restored values are there
     griddep_launch_dependents();
     constexpr int Q4 = D / 32;
+    constexpr int kBatch = kRows * D > 64 ? 2 : 4;
     __shared__ float4 part[2][kWarps][kRows][D / 4];
     __shared__ float part_s[kWarps][kRows][3];  // maximum, sum e, sum e dp
     const int R = G * T;
@@ -74,38 +78,60 @@ ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* _
         }
     }
     const int total = n + last + 1;
-    for (int u0 = warp * 4; u0 < total; u0 += kWarps * 4) {
-        const int u = u0 + sub;
-        const int uu = min(u, total - 1);
-        const E* kp = uu < n ? K + (bg * pitch + uu) * D : k + (bg * T + (uu - n)) * D;
-        const E* vp = uu < n ? V + (bg * pitch + uu) * D : v + (bg * T + (uu - n)) * D;
-        float4 kk[Q4], vv[Q4];
+    for (int u0 = warp * 4; u0 < total; u0 += kStride * kBatch) {
+        float4 kk[kBatch][Q4], vv[kBatch][Q4];
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) kk[c] = load4(kp + 32 * c + 4 * l8);
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = min(u0 + kStride * b + sub, total - 1);
+            const size_t at = u < n ? (bg * pitch + u) * D : (bg * T + (u - n)) * D;
+            const E *kp = (u < n ? K : k) + at, *vp = (u < n ? V : v) + at;
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) vv[c] = load4(vp + 32 * c + 4 * l8);
+            for (int c = 0; c < Q4; ++c) kk[b][c] = load4(kp + 32 * c + 4 * l8);
+#pragma unroll
+            for (int c = 0; c < Q4; ++c) vv[b][c] = load4(vp + 32 * c + 4 * l8);
+        }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            float s = 0.f, dp = 0.f;
+            float s[kBatch], dp[kBatch];
+            bool see[kBatch];
 #pragma unroll
-            for (int c = 0; c < Q4; ++c) {
-                s = dot4(qr[r][c], kk[c], s);
-                dp = dot4(dr[r][c], vv[c], dp);
-            }
-            s = sum8(s) * scale_log2;
-            dp = sum8(dp);
-            if (u < total && u - n <= tok[r]) {
-                const float mn = fmaxf(m[r], s);
-                const float a = exp2f(m[r] - mn), e = exp2f(s - mn), ed = e * dp;
-                l[r] = fmaf(l[r], a, e);
-                w[r] = fmaf(w[r], a, ed);
-                m[r] = mn;
+            for (int b = 0; b < kBatch; ++b) {
+                s[b] = dp[b] = 0.f;
 #pragma unroll
                 for (int c = 0; c < Q4; ++c) {
-                    A[r][c] = fma4(ed, kk[c], scale4(A[r][c], a));
-                    Z[r][c] = fma4(e, kk[c], scale4(Z[r][c], a));
+                    s[b] = dot4(qr[r][c], kk[b][c], s[b]);
+                    dp[b] = dot4(dr[r][c], vv[b][c], dp[b]);
                 }
+                const int u = u0 + kStride * b + sub;
+                see[b] = u < total && u - n <= tok[r];
+                s[b] = sum8(s[b]);
+                s[b] = see[b] ? s[b] * scale_log2 : -INFINITY;
+                dp[b] = sum8(dp[b]);
             }
+            float mn = m[r];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) mn = fmaxf(mn, s[b]);
+            const float ms = mn == -INFINITY ? 0.f : mn, a = exp2f(m[r] - ms);
+            m[r] = mn;
+            l[r] *= a;
+            w[r] *= a;
+#pragma unroll
+            for (int c = 0; c < Q4; ++c) {
+                A[r][c] = scale4(A[r][c], a);
+                Z[r][c] = scale4(Z[r][c], a);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (see[b]) {
+                    const float e = exp2f(s[b] - ms), ed = e * dp[b];
+                    l[r] += e;
+                    w[r] += ed;
+#pragma unroll
+                    for (int c = 0; c < Q4; ++c) {
+                        A[r][c] = fma4(ed, kk[b][c], A[r][c]);
+                        Z[r][c] = fma4(e, kk[b][c], Z[r][c]);
+                    }
+                }
         }
     }
 #pragma unroll
@@ -155,13 +181,14 @@ ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* _
 // gradients from n on), u >= C is chunk token u - C. Eight lanes share a query
 // row, the CTA takes 32 rows at a time.
 template <typename E, int D, int kKeys>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, D == 64 ? 2 : 1)
 ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
                       const E* __restrict__ V, const E* __restrict__ dout, const float4* __restrict__ stats,
                       E* __restrict__ dK, E* __restrict__ dV, E* __restrict__ dk, E* __restrict__ dv, int G, int C, int T,
                       int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
     griddep_wait();  // the statistics are there
     constexpr int Q4 = D / 32;
+    constexpr int kBatch = kKeys * D > 64 ? 2 : 4;
     __shared__ float4 part[2][kWarps][kKeys][D / 4];
     const int R = G * T;
     const size_t bg = blockIdx.x / blocks_per_group;
@@ -187,33 +214,39 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
         }
     }
     const int span = T - first;  // rows of each head from `first` on
-    for (int x0 = warp * 4; x0 < G * span; x0 += kWarps * 4) {
-        const int x = min(x0 + sub, G * span - 1);
-        const int i = first + x % span;
-        const size_t row = bg * R + (size_t)(x / span) * T + i;
-        const bool in = x0 + sub < G * span;
-        float4 qq[Q4], dd[Q4];
+    for (int x0 = warp * 4; x0 < G * span; x0 += kStride * kBatch) {
+        float4 qq[kBatch][Q4], dd[kBatch][Q4], st[kBatch];
+        int tok[kBatch];  // -1: no row
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) qq[c] = load4(q + row * D + 32 * c + 4 * l8);
+        for (int b = 0; b < kBatch; ++b) {
+            const int x = min(x0 + kStride * b + sub, G * span - 1), head = x / span, i = first + x - head * span;
+            const size_t row = bg * R + (size_t)head * T + i;
+            tok[b] = x0 + kStride * b + sub < G * span ? i : -1;
 #pragma unroll
-        for (int c = 0; c < Q4; ++c) dd[c] = load4(dout + row * D + 32 * c + 4 * l8);
-        const float4 st = stats[row];
+            for (int c = 0; c < Q4; ++c) qq[b][c] = load4(q + row * D + 32 * c + 4 * l8);
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            float s = 0.f, dp = 0.f;
+            for (int c = 0; c < Q4; ++c) dd[b][c] = load4(dout + row * D + 32 * c + 4 * l8);
+            st[b] = stats[row];
+        }
 #pragma unroll
-            for (int c = 0; c < Q4; ++c) {
-                s = dot4(qq[c], kr[j][c], s);
-                dp = dot4(dd[c], vr[j][c], dp);
-            }
-            s = sum8(s) * scale_log2;
-            dp = sum8(dp);
-            if (in && i >= from[j]) {
-                const float p = exp2f(s - st.x) * st.y, ds = p * (dp - st.z);
+        for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                float s = 0.f, dp = 0.f;
 #pragma unroll
                 for (int c = 0; c < Q4; ++c) {
-                    gv[j][c] = fma4(p, dd[c], gv[j][c]);
-                    gk[j][c] = fma4(ds, qq[c], gk[j][c]);
+                    s = dot4(qq[b][c], kr[j][c], s);
+                    dp = dot4(dd[b][c], vr[j][c], dp);
+                }
+                s = sum8(s) * scale_log2;
+                dp = sum8(dp);
+                if (tok[b] >= from[j]) {
+                    const float p = exp2f(s - st[b].x) * st[b].y, ds = p * (dp - st[b].z);
+#pragma unroll
+                    for (int c = 0; c < Q4; ++c) {
+                        gv[j][c] = fma4(p, dd[b][c], gv[j][c]);
+                        gk[j][c] = fma4(ds, qq[b][c], gk[j][c]);
+                    }
                 }
             }
         }
