@@ -27,9 +27,10 @@
 // Bound by the tensor core: 2 products of 2 d per visible (row, key) for the
 // statistics, 4 for dQ and 4 for dK and dV. An operand pair from shared memory needs
 // 128 bytes a clock at the MMA's full rate, all there is, so P and dS stay in
-// TMEM (64 bytes a clock), and they never cross shared memory. Ten warps: a TMA
-// loader, an MMA issuer and two warpgroups that share every tile, one half of
-// its columns each. The issue order keeps the tensor core on a product that
+// TMEM (64 bytes a clock), and they never cross shared memory. A TMA loader, an MMA
+// issuer and four warpgroups that share every tile, 32 of its columns each (two with
+// 64: 202 us a pass at T=1024 C=2048 d=128 and 49 at B=2 T=333 C=1000 d=64; four: 197
+// and 47). The issue order keeps the tensor core on a product that
 // does not wait for the exponentials in progress: dV(t), S(t+1) while dS(t) is
 // computed, dK(t), dP(t+1) while P(t+1) is.
 //
@@ -54,8 +55,9 @@ using tc::ex2;
 using tc::fence_after_sync;
 using tc::fence_before_sync;
 
-constexpr int kThreads = 320;   // loader, MMA issuer, two warpgroups
-constexpr int kConsumers = 256;
+constexpr int kGroups = 4;  // warpgroups that share a tile, 32 of its columns each
+constexpr int kConsumers = 128 * kGroups, kThreads = 64 + kConsumers;  // and a loader and an MMA issuer
+constexpr int kArrivals = kConsumers / 32;
 constexpr int kMaxCluster = 4;
 
 struct CkptTcParams {
@@ -88,16 +90,16 @@ __device__ __forceinline__ int chunk_blocks(const CkptTcParams& p, int tile) {
     return (r1 / p.T > r0 / p.T ? p.T - 1 : r1 % p.T) / 128 + 1;
 }
 
-// What rounding to the packed bf16 `hi` left of 64 values, as bf16, to 32 columns.
-__device__ __forceinline__ void store_rest(uint32_t taddr, const uint32_t (&x)[2][32], const uint32_t (&hi)[32]) {
-    uint32_t lo[32];
+// What rounding to the packed bf16 `hi` left of 32 values, as bf16, to 16 columns.
+__device__ __forceinline__ void store_rest(uint32_t taddr, const uint32_t (&x)[32], const uint32_t (&hi)[16]) {
+    uint32_t lo[16];
 #pragma unroll
-    for (int e = 0; e < 64; e += 2) {
+    for (int e = 0; e < 32; e += 2) {
         const uint32_t h = hi[e >> 1];
-        lo[e >> 1] = tc::pack_bf16(__uint_as_float(x[e >> 5][e & 31]) - __uint_as_float(h << 16),
-                                   __uint_as_float(x[e >> 5][(e & 31) + 1]) - __uint_as_float(h & 0xffff0000u));
+        lo[e >> 1] = tc::pack_bf16(__uint_as_float(x[e]) - __uint_as_float(h << 16),
+                                   __uint_as_float(x[e + 1]) - __uint_as_float(h & 0xffff0000u));
     }
-    tc::tmem_st32(taddr, lo);
+    tc::tmem_st16(taddr, lo);
 }
 
 // ============================================================================
@@ -111,8 +113,7 @@ struct DqCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_DO = TILE;
     static constexpr int OFF_RING = 2 * TILE;
-    static constexpr int OFF_ST = OFF_RING + RING * TILE;  // [3][128] floats
-    static constexpr int OFF_BAR = OFF_ST + 3 * 128 * 4;
+    static constexpr int OFF_BAR = OFF_RING + RING * TILE;
     static constexpr int NBAR = 24;
     static constexpr int SMEM_RAW = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr int SMEM = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;  // one CTA (512 TMEM columns) per SM
@@ -135,10 +136,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
     uint64_t* ring_full = bars + 1;           // [RING]
     uint64_t* ring_empty = ring_full + RING;  // [RING]
     uint64_t* sd_full = ring_empty + RING;    // [2] pass 1: S and dP of a buffer
-    uint64_t* sd_free = sd_full + 2;          // [2] pass 1, 8 arrivals: in registers
+    uint64_t* sd_free = sd_full + 2;          // [2] pass 1, kArrivals: in registers
     uint64_t* s_full = sd_free + 2;           // [2] pass 2: S of a buffer
     uint64_t* dp_full = s_full + 2;           // pass 2: dP
-    uint64_t* ds_full = dp_full + 1;          // pass 2, 8 arrivals: dS over S, dP in registers
+    uint64_t* ds_full = dp_full + 1;          // pass 2, kArrivals: dS over S, dP in registers
     uint64_t* drain = ds_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -162,11 +163,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(sd_full + b, 1);
-            mbar_init(sd_free + b, 8);
+            mbar_init(sd_free + b, kArrivals);
             mbar_init(s_full + b, 1);
         }
         mbar_init(dp_full, 1);
-        mbar_init(ds_full, 8);
+        mbar_init(ds_full, kArrivals);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -278,11 +279,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
             const int ks = 2 * t % RING;
             const uint64_t b = dRingN + (uint64_t)((ks * Cfg::TILE) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {  // 16 keys at a time; the keys' halves at columns 0 and 64, each hi and lo
-                const uint32_t a = tmem + 128 * (t & 1) + 64 * (kk >> 2) + 8 * (kk & 3);
+            for (int kk = 0; kk < 8; ++kk) {  // 16 keys at a time; every 32 keys at their columns, hi and lo
+                const uint32_t a = tmem + 128 * (t & 1) + 32 * (kk >> 1) + 8 * (kk & 1);
                 const uint64_t bk = b + (uint64_t)((kk * 16 * 128) >> 4);
                 tc::mma_bf16_ts_warp(tmem + 384, a, bk, Cfg::IDESC_G, (t > 0 || kk > 0) ? 1u : 0u);
-                tc::mma_bf16_ts_warp(tmem + 384, a + 32, bk, Cfg::IDESC_G, 1u);
+                tc::mma_bf16_ts_warp(tmem + 384, a + 16, bk, Cfg::IDESC_G, 1u);
             }
             tc::mma_commit_warp(ring_empty + ks);
             if (t + 2 < n2) ok = issue_s(t + 2);
@@ -293,16 +294,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
         warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
     } else {
         // ---------------------------------------------------------- row warpgroups
-        const int wg = (warp - 2) >> 2;  // columns 64 wg .. 64 wg + 63
+        const int wg = (warp - 2) >> 2;  // columns 32 wg .. 32 wg + 31
         const int quad = warp & 3;
         const int r = quad * 32 + lane;  // row inside the tile = TMEM lane
-        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + 64 * wg;
-        float* st = reinterpret_cast<float*>(smem + Cfg::OFF_ST);
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + 32 * wg;
         const int token = (m0 + r) % p.T;
-        // visible columns of this row's half in this CTA's block t: e < limit
+        // visible columns of this thread's in this CTA's block t: e < limit
         auto limit_of = [&](int t) {
             const int j = jb + t;
-            return (j < p.nbc ? p.n - 128 * j : token - 128 * (j - p.nbc) + 1) - 64 * wg;
+            return (j < p.nbc ? p.n - 128 * j : token - 128 * (j - p.nbc) + 1) - 32 * wg;
         };
         float m = -INFINITY, l = 0.f, w = 0.f;
         bool ok = true;
@@ -310,45 +310,40 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
             const int b = t & 1;
             if (!(ok = warp_wait(sd_full + b, (t >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
-            uint32_t s[2][32], dp[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tl + 128 * b + 32 * c, s[c]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tl + 256 + 128 * b + 32 * c, dp[c]);
+            uint32_t s[32], dp[32];
+            tc::tmem_ld32(tl + 128 * b, s);
+            tc::tmem_ld32(tl + 256 + 128 * b, dp);
             tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                tc::reg_fence(s[c]);
-                tc::reg_fence(dp[c]);
-            }
+            tc::reg_fence(s);
+            tc::reg_fence(dp);
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(sd_free + b);
             const int limit = limit_of(t);
-            if (limit < 64) {
+            if (limit < 32) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e >= limit) s[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < 32; ++e)
+                    if (e >= limit) s[e] = __float_as_uint(-INFINITY);
             }
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                mx0 = tc::max3(mx0, __uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
-                mx1 = tc::max3(mx1, __uint_as_float(s[e >> 5][(e & 31) + 2]), __uint_as_float(s[e >> 5][(e & 31) + 3]));
+            for (int e = 0; e < 32; e += 4) {
+                mx0 = tc::max3(mx0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                mx1 = tc::max3(mx1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
             }
             const float mn = fmaxf(m, fmaxf(mx0, mx1) * p.scale_log2);
-            const float ms = mn == -INFINITY ? 0.f : mn;  // no visible key in this half yet
+            const float ms = mn == -INFINITY ? 0.f : mn;  // no visible key in these columns yet
             const float a = ex2(m - ms);
             m = mn;
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ms, -ms);
             float2 l2 = make_float2(0.f, 0.f), w2 = l2;
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < 32; e += 2) {
                 const float2 x = tc::ffma2(
-                    make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), sc2, nm2);
+                    make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nm2);
                 const float2 pe = make_float2(ex2(x.x), ex2(x.y));
                 l2 = tc::fadd2(l2, pe);
-                w2 = tc::ffma2(pe, make_float2(__uint_as_float(dp[e >> 5][e & 31]), __uint_as_float(dp[e >> 5][(e & 31) + 1])), w2);
+                w2 = tc::ffma2(pe, make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), w2);
             }
             l = fmaf(l, a, l2.x + l2.y);
             w = fmaf(w, a, w2.x + w2.y);
@@ -356,18 +351,23 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
         const bool row_ok = m0 + r < p.R;
         const size_t at = ((size_t)bg * p.tiles + tile) * 128 + r, all_rows = (size_t)groups * p.tiles * 128;
         if (pass1) {
-            // the two halves of a row meet
-            if (wg == 1) {
-                st[r] = m;
-                st[128 + r] = l;
-                st[256 + r] = w;
-            }
+            // the quarters of a row meet, in the ring: every key block has been multiplied
+            float* st = reinterpret_cast<float*>(smem + Cfg::OFF_RING);  // [kGroups][3][128]
+            st[384 * wg + r] = m;
+            st[384 * wg + 128 + r] = l;
+            st[384 * wg + 256 + r] = w;
             tc::named_sync(1, kConsumers);
             if (wg == 0) {
-                float M = fmaxf(m, st[r]);
-                float Ms = M == -INFINITY ? 0.f : M;
-                const float a0 = ex2(m - Ms), a1 = ex2(st[r] - Ms);
-                float L = l * a0 + st[128 + r] * a1, W = w * a0 + st[256 + r] * a1;
+                float M = m;
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g) M = fmaxf(M, st[384 * g + r]);
+                float Ms = M == -INFINITY ? 0.f : M, L = 0.f, W = 0.f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const float a = ex2(st[384 * g + r] - Ms);
+                    L = fmaf(st[384 * g + 128 + r], a, L);
+                    W = fmaf(st[384 * g + 256 + r], a, W);
+                }
                 bool mine = true;
                 if (p.parts > 1) {
                     // the tile's last CTA adds up its parts, in order
@@ -407,44 +407,39 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
             const uint32_t tS = tl + 128 * (t & 1);
             if (!(ok = warp_wait(s_full + (t & 1), (t >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
-            uint32_t s[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tS + 32 * c, s[c]);
+            uint32_t s[32];
+            tc::tmem_ld32(tS, s);
             tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::reg_fence(s[c]);
+            tc::reg_fence(s);
             const int limit = limit_of(t);
-            if (limit < 64) {
+            if (limit < 32) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e >= limit) s[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < 32; ++e)
+                    if (e >= limit) s[e] = __float_as_uint(-INFINITY);
             }
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < 32; e += 2) {
                 const float2 x = tc::ffma2(
-                    make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), sc2, nl2);
-                s[e >> 5][e & 31] = __float_as_uint(ex2(x.x));
-                s[e >> 5][(e & 31) + 1] = __float_as_uint(ex2(x.y));
+                    make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nl2);
+                s[e] = __float_as_uint(ex2(x.x));
+                s[e + 1] = __float_as_uint(ex2(x.y));
             }
             if (!(ok = warp_wait(dp_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
+            uint32_t dp[32], hi[16], lo[16];
+            tc::tmem_ld32(tl + 256, dp);
+            tc::tmem_ld_wait();
+            tc::reg_fence(dp);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t dp[32], hi[16], lo[16];
-                tc::tmem_ld32(tl + 256 + 32 * c, dp);
-                tc::tmem_ld_wait();
-                tc::reg_fence(dp);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 y = tc::fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd2);
-                    const float a = __uint_as_float(s[c][e]) * y.x, b = __uint_as_float(s[c][e + 1]) * y.y;
-                    const uint32_t h = tc::pack_bf16(a, b);
-                    hi[e >> 1] = h;
-                    lo[e >> 1] = tc::pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-                }
-                tc::tmem_st16(tS + 16 * c, hi);
-                tc::tmem_st16(tS + 32 + 16 * c, lo);
+            for (int e = 0; e < 32; e += 2) {
+                const float2 y = tc::fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd2);
+                const float a = __uint_as_float(s[e]) * y.x, b = __uint_as_float(s[e + 1]) * y.y;
+                const uint32_t h = tc::pack_bf16(a, b);
+                hi[e >> 1] = h;
+                lo[e >> 1] = tc::pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
             }
+            tc::tmem_st16(tS, hi);
+            tc::tmem_st16(tS + 16, lo);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -452,30 +447,30 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& map_q, const CUtensorM
         }
         if (ok) ok = warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
         fence_after_sync();
-        // dQ: this thread has D / 2 columns of its row. A part goes to memory as it is,
+        // dQ: this thread has D / 4 columns of its row. A part goes to memory as it is,
         // rows next to each other; the whole goes through shared memory (the key ring is
         // done with), 16-byte chunks permuted by the row so that no bank is met twice
-        constexpr int kCols = D / 2;
+        constexpr int kCols = D / kGroups;
         const int col0 = kCols * wg;
-        const uint32_t tQ = tmem + ((uint32_t)(quad * 32) << 16) + 384 + col0;
         float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_RING);
         if (pass2 && ok) {
-#pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-                uint32_t o[32];
-                tc::tmem_ld32(tQ + c, o);
-                tc::tmem_ld_wait();
-                tc::reg_fence(o);
-                float4* dst = p.part + ((((size_t)part * groups + bg) * p.tiles + tile) * (D / 4) + (col0 + c) / 4) * 128 + r;
+            uint32_t o[kCols];
+            const uint32_t tQ = tmem + ((uint32_t)(quad * 32) << 16) + 384 + col0;
+            if constexpr (kCols == 32)
+                tc::tmem_ld32(tQ, o);
+            else
+                tc::tmem_ld16(tQ, o);
+            tc::tmem_ld_wait();
+            tc::reg_fence(o);
+            float4* dst = p.part + ((((size_t)part * groups + bg) * p.tiles + tile) * (D / 4) + col0 / 4) * 128 + r;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                                 __uint_as_float(o[e + 3]));
-                    if (p.parts > 1)
-                        dst[e / 4 * 128] = x;
-                    else
-                        *reinterpret_cast<float4*>(acc + r * D + (((col0 + c + e) / 4) ^ (r & (D / 4 - 1))) * 4) = x;
-                }
+            for (int e = 0; e < kCols; e += 4) {
+                const float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                             __uint_as_float(o[e + 3]));
+                if (p.parts > 1)
+                    dst[e / 4 * 128] = x;
+                else
+                    *reinterpret_cast<float4*>(acc + r * D + (((col0 + e) / 4) ^ (r & (D / 4 - 1))) * 4) = x;
             }
         }
         if (pass2 && p.parts == 1) {
@@ -551,9 +546,9 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
     uint64_t* t_full = bars + 1;   // [2] a query tile has landed
     uint64_t* t_empty = bars + 3;  // [2] its MMAs have completed
     uint64_t* s_full = bars + 5;   // S^T
-    uint64_t* p_full = bars + 6;   // 8 arrivals: P^T over S^T
+    uint64_t* p_full = bars + 6;   // kArrivals: P^T over S^T
     uint64_t* dp_full = bars + 7;  // dP^T
-    uint64_t* ds_full = bars + 8;  // 8 arrivals: dS^T over dP^T
+    uint64_t* ds_full = bars + 8;  // kArrivals: dS^T over dP^T
     uint64_t* drain = bars + 9;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -594,9 +589,9 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
             mbar_init(t_empty + s, 1);
         }
         mbar_init(s_full, 1);
-        mbar_init(p_full, 8);
+        mbar_init(p_full, kArrivals);
         mbar_init(dp_full, 1);
-        mbar_init(ds_full, 8);
+        mbar_init(ds_full, kArrivals);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -664,13 +659,13 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
         };
         auto issue_ts = [&](uint32_t acc, uint32_t a, uint64_t b, bool first) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 rows at a time; the rows' halves at columns 0 and 64
-                tc::mma_bf16_ts_warp(acc, a + 64 * (kk >> 2) + 8 * (kk & 3), b + (uint64_t)((kk * 16 * 128) >> 4),
+            for (int kk = 0; kk < 8; ++kk)  // 16 rows at a time; every 32 rows at their columns
+                tc::mma_bf16_ts_warp(acc, a + 32 * (kk >> 1) + 8 * (kk & 1), b + (uint64_t)((kk * 16 * 128) >> 4),
                                      Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
             if (p.pairs) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_bf16_ts_warp(acc, a + 32 + 64 * (kk >> 2) + 8 * (kk & 3), b + (uint64_t)((kk * 16 * 128) >> 4),
+                    tc::mma_bf16_ts_warp(acc, a + 16 + 32 * (kk >> 1) + 8 * (kk & 1), b + (uint64_t)((kk * 16 * 128) >> 4),
                                          Cfg::IDESC_G, 1u);
             }
         };
@@ -710,51 +705,46 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
         warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
     } else {
         // ---------------------------------------------------------- key warpgroups
-        const int wg = (warp - 2) >> 2;  // rows 64 wg .. 64 wg + 63 of a tile
+        const int wg = (warp - 2) >> 2;  // rows 32 wg .. 32 wg + 31 of a tile
         const int quad = warp & 3;
         const int kr = quad * 32 + lane;  // key inside the block = TMEM lane
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        const uint32_t tl = tmem + lane_off + 64 * wg;
+        const uint32_t tl = tmem + lane_off + 32 * wg;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         int t = 0;
         for (int tile = first; tile < p.tiles; tile = next(tile, ranks), ++t) {
             // the rows' statistics came with the tile
-            const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROW + (t & 1) * 1024) + 64 * wg;
+            const float* rows = reinterpret_cast<const float*>(smem + Cfg::OFF_ROW + (t & 1) * 1024) + 32 * wg;
             if (!(ok = warp_wait(t_full + (t & 1), (t >> 1) & 1, p.wb, kDevTimeoutTmaWait, abort_flag) &&
                        warp_wait(s_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag)))
                 break;
             fence_after_sync();
-            uint32_t s[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::tmem_ld32(tl + 32 * c, s[c]);
+            uint32_t s[32];
+            tc::tmem_ld32(tl, s);
             tc::tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tc::reg_fence(s[c]);
+            tc::reg_fence(s);
             // a chunk key is seen by the tokens from its own on: unless every row of the
             // tile is one, each is compared (a tile may hold the end of one head and the
             // start of another, or several heads)
             if (!cache) {
                 const int i0 = 128 * tile % p.T;
                 if (i0 + 127 >= p.T || i0 < t0 + 127) {
-                    uint32_t vis[2] = {0u, 0u};
-                    for (int c = -((i0 + 64 * wg) % p.T); c < 64; c += p.T) {  // a head starts at column c
-                        const int lo = max(c + t0 + kr, 0), hi = min(c + p.T, 64);
-                        if (lo >= hi) continue;
-                        const unsigned long long ones = (~0ull >> (64 - (hi - lo))) << lo;
-                        vis[0] |= (uint32_t)ones;
-                        vis[1] |= (uint32_t)(ones >> 32);
+                    uint32_t vis = 0;
+                    for (int c = -((i0 + 32 * wg) % p.T); c < 32; c += p.T) {  // a head starts at column c
+                        const int lo = max(c + t0 + kr, 0), hi = min(c + p.T, 32);
+                        if (lo < hi) vis |= (~0u >> (32 - (hi - lo))) << lo;
                     }
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (!((vis[e >> 5] >> (e & 31)) & 1u)) s[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+                    for (int e = 0; e < 32; ++e)
+                        if (!((vis >> e) & 1u)) s[e] = __float_as_uint(-INFINITY);
                 }
             }
-            uint32_t pk[32];
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
                 const float4 nl = *reinterpret_cast<const float4*>(rows + e);
-                uint32_t* x = &s[e >> 5][e & 31];
+                uint32_t* x = &s[e];
                 const float2 a = tc::ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, make_float2(nl.x, nl.y));
                 const float2 b = tc::ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, make_float2(nl.z, nl.w));
                 const float2 pa = make_float2(ex2(a.x), ex2(a.y)), pb = make_float2(ex2(b.x), ex2(b.y));
@@ -765,33 +755,30 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
                 pk[e >> 1] = tc::pack_bf16(pa.x, pa.y);
                 pk[(e >> 1) + 1] = tc::pack_bf16(pb.x, pb.y);
             }
-            tc::tmem_st32(tl, pk);
-            if (p.pairs) store_rest(tl + 32, s, pk);
+            tc::tmem_st16(tl, pk);
+            if (p.pairs) store_rest(tl + 16, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full);
             if (!(ok = warp_wait(dp_full, t & 1, p.wb, kDevTimeoutMmaWait, abort_flag))) break;
             fence_after_sync();
+            uint32_t dp[32];
+            tc::tmem_ld32(tl + 128, dp);
+            tc::tmem_ld_wait();
+            tc::reg_fence(dp);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t dp[32];
-                tc::tmem_ld32(tl + 128 + 32 * c, dp);
-                tc::tmem_ld_wait();
-                tc::reg_fence(dp);
+            for (int e = 0; e < 32; e += 4) {
+                const float4 dr = *reinterpret_cast<const float4*>(rows + 128 + e);
+                const float d4[4] = {dr.x, dr.y, dr.z, dr.w};
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 dr = *reinterpret_cast<const float4*>(rows + 128 + 32 * c + e);
-                    const float d4[4] = {dr.x, dr.y, dr.z, dr.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        s[c][e + x] = __float_as_uint(__uint_as_float(s[c][e + x]) * (__uint_as_float(dp[e + x]) - d4[x]));
-                    pk[16 * c + (e >> 1)] = tc::pack_bf16(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                    pk[16 * c + (e >> 1) + 1] = tc::pack_bf16(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]));
-                }
+                for (int x = 0; x < 4; ++x)
+                    s[e + x] = __float_as_uint(__uint_as_float(s[e + x]) * (__uint_as_float(dp[e + x]) - d4[x]));
+                pk[e >> 1] = tc::pack_bf16(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                pk[(e >> 1) + 1] = tc::pack_bf16(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
             }
-            tc::tmem_st32(tl + 128, pk);
-            if (p.pairs) store_rest(tl + 160, s, pk);
+            tc::tmem_st16(tl + 128, pk);
+            if (p.pairs) store_rest(tl + 144, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -799,14 +786,14 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
         }
         if (ok && warp_wait(drain, 0, p.wb, kDevTimeoutMmaWait, abort_flag)) {
             fence_after_sync();
-            // into shared memory, where the query tiles were: dV by the first warpgroup,
-            // dK by the second; 16-byte chunks of a row are permuted by the row, so that
+            // into shared memory, where the query tiles were: dV by the first two warpgroups,
+            // dK by the others, half of the columns each; 16-byte chunks of a row are permuted by the row, so that
             // neither these stores nor the loads below meet in a bank
-            float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_T) + (wg * 128 + kr) * D;
+            float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_T) + (wg / 2 * 128 + kr) * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = wg % 2 * (D / 2); c < (wg % 2 + 1) * (D / 2); c += 32) {
                 uint32_t o[32];
-                tc::tmem_ld32(tmem + lane_off + 256 + wg * D + c, o);
+                tc::tmem_ld32(tmem + lane_off + 256 + wg / 2 * D + c, o);
                 tc::tmem_ld_wait();
                 tc::reg_fence(o);
 #pragma unroll
