@@ -7,7 +7,9 @@
 // head. The blocks of all units form one line that is divided evenly over the
 // SMs, one CTA each, so a CTA works on the end of one unit, whole units, and the
 // start of another; a part of a unit leaves its unnormalised output, maximum and
-// sum in fp32, and tree_combine_kernel merges the parts in order.
+// sum in fp32, and tree_combine_kernel merges the parts in order. Where it costs no
+// more blocks, a unit's CTAs are a cluster, keep their parts in shared memory and merge
+// them there.
 //
 // Per block and tile: S = Q K^T in TMEM; two threads per row take 64 columns each
 // into registers, exchange their maxima, and write P = 2^(s - m) back over S as
@@ -32,6 +34,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "kernels.h"
 #include "operators.h"
@@ -50,6 +55,7 @@ using tc::fence_before_sync;
 // exponents, and O and the sum are fp32.
 constexpr float kRescale = 16.f;
 constexpr int kUnitRows = 256;
+constexpr int kMaxCluster = 8;
 
 template <int D>
 struct TreeCfg {
@@ -98,6 +104,7 @@ struct TreeParams {
     float4* part_o;  // [2 CTAs][D / 4][256]: four columns of a row together, rows next to each other
     unsigned* count; // [KV heads], zero: CTAs that have left their part (nullptr: merged by a kernel of its own)
     float2* part_ml; // [2 CTAs][256]: log2-domain maximum (NaN: the row's node is absent) and sum
+    int cluster;     // > 0: a unit's CTAs, a cluster of as many, merge it in shared memory
     WaitBound wb;
 };
 
@@ -173,6 +180,50 @@ __device__ __forceinline__ void merge_row(const TreeParams& p, unsigned bg, int 
     const size_t at = (size_t)bg * p.R + row;
     *reinterpret_cast<uint2*>(p.out + at * D + 4 * col4) = h;
     if (col4 == 0) p.lse[at] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// The same for a unit whose parts lie in the shared memory of a cluster: each CTA merges
+// its share of the rows. `acc`, `ml`: shared addresses of a part's rows and of their
+// maxima and sums.
+template <int D>
+__device__ __forceinline__ void merge_cluster(const TreeParams& p, const Segment& s, uint32_t acc, uint32_t ml) {
+    constexpr int kLanes = D / 4, kPerWarp = 32 / kLanes;  // lanes per row, rows per warp
+    const int rank = tc::cluster_rank(), warp = threadIdx.x / 32, lane = threadIdx.x % 32, c4 = lane % kLanes;
+    const int end = s.rows * (rank + 1) / p.cluster;
+    for (int r = s.rows * rank / p.cluster + warp * kPerWarp + lane / kLanes; r < end; r += TreeCfg<D>::THREADS / 32 * kPerWarp) {
+        float2 x[kMaxCluster];
+        float4 o[kMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q >= p.cluster) break;
+            const float4 s4 = tc::cluster_load4(ml + 16 * r, q);
+            x[q] = make_float2(s4.x, s4.y);
+            o[q] = tc::cluster_load4(acc + (r * D + (c4 ^ (r & (kLanes - 1))) * 4) * 4, q);
+        }
+        float M = -INFINITY, L = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool absent = false;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q >= p.cluster) break;
+            absent |= x[q].x != x[q].x;
+            M = fmaxf(M, x[q].x);
+        }
+        const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q >= p.cluster) break;
+            const float w = ex2(x[q].x - ms);
+            L = fmaf(x[q].y, w, L);
+            a = make_float4(fmaf(o[q].x, w, a.x), fmaf(o[q].y, w, a.y), fmaf(o[q].z, w, a.z), fmaf(o[q].w, w, a.w));
+        }
+        const float inv = 1.f / L;
+        uint2 out = make_uint2(tc::pack_bf16(a.x * inv, a.y * inv), tc::pack_bf16(a.z * inv, a.w * inv));
+        if (absent) out = make_uint2(0, 0);
+        const size_t at = (size_t)s.bg * p.R + s.m0 + r;
+        *reinterpret_cast<uint2*>(p.out + at * D + 4 * c4) = out;
+        if (c4 == 0) p.lse[at] = absent ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
 }
 
 template <int D>
@@ -574,8 +625,33 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             l += xl[128 - 128 * h];
             tc::named_sync(1 + X, 256);
             if (ok) ok = warp_wait(o_full + X, done++ & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
+            // the other tile's products too: what follows overwrites their operands
+            if (p.cluster && s.hasB && ok) ok = warp_wait(o_full + 1 - X, 0, p.wb, kDevTimeoutMmaWait, abort_flag);
             fence_after_sync();
-            if (busy && ok) {
+            if (p.cluster) {
+                if (busy && ok) {
+                    // to shared memory, 16-byte chunks of a row permuted by the row, so that
+                    // neither these stores nor the merge's loads meet in a bank
+                    float* acc = reinterpret_cast<float*>(smem + Cfg::OFF_RING) + (128 * X + r) * D;
+#pragma unroll 1
+                    for (int x = 0; x < D / 2; x += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + x, o);
+                        tc::tmem_ld_wait();
+                        tc::reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const int chunk = (h * (D / 2) + x + e) / 4;
+                            uint4 w = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            if (spoilt) w.x = w.y = w.z = w.w = 0x7fffffffu;
+                            *reinterpret_cast<uint4*>(acc + (chunk ^ (r & (D / 4 - 1))) * 4) = w;
+                        }
+                    }
+                    if (h == 0)
+                        reinterpret_cast<float4*>(smem + Cfg::OFF_Q)[128 * X + r] =
+                            make_float4(absent ? __uint_as_float(0x7fffffffu) : m, l, 0.f, 0.f);
+                }
+            } else if (busy && ok) {
                 const float nan = __uint_as_float(0x7fffffffu);
                 const bool row_ok = row < p.R;
                 const size_t part = 2 * blockIdx.x + (s.first ? 0 : 1);
@@ -634,10 +710,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         }
     }
     fence_before_sync();
-    __syncthreads();
+    if (p.cluster) {
+        __syncwarp();
+        tc::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
+    }
+    if (p.cluster) {
+        merge_cluster<D>(p, segment(p, w0, w0, w1), sbase + Cfg::OFF_RING, sbase + Cfg::OFF_Q);
+        tc::cluster_sync();  // no CTA leaves while another reads its part
     }
 }
 
@@ -652,6 +737,35 @@ tree_combine_kernel(const TreeParams p, unsigned rows) {
     constexpr unsigned kRows = 1024 / D;
     const unsigned g = blockIdx.x * kRows + threadIdx.x % kRows;
     if (g < rows) merge_row<D>(p, g / (unsigned)p.R, (int)(g % (unsigned)p.R), threadIdx.x / kRows);
+}
+
+// Clusters of k CTAs that can be on the device at once (an SM takes one CTA, and a
+// cluster stays inside one part of the device).
+template <int D>
+cudaError_t clusters_at_once(int k, int* clusters) {
+    static std::mutex mu;
+    static std::map<std::pair<int, int>, int> known;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto at = known.find({dev, k});
+    if (at != known.end()) {
+        *clusters = at->second;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(k);
+    cfg.blockDim = dim3(TreeCfg<D>::THREADS);
+    cfg.dynamicSmemBytes = TreeCfg<D>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = k;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaError_t e = cudaOccupancyMaxActiveClusters(clusters, tree_tc_kernel<D>, &cfg); e != cudaSuccess) return e;
+    known[{dev, k}] = *clusters;
+    return cudaSuccess;
 }
 
 template <int D>
@@ -677,14 +791,27 @@ cudaError_t tree_launch(const TreeArgs& a) {
     const long long total = (long long)groups * p.pairs * p.nb;
     if (total >= 1ll << 31) return cudaErrorInvalidValue;  // a cache of this many blocks does not fit the card
     // The line is divided evenly, or every unit among the same number of CTAs: then
-    // fewer CTAs may work, but each leaves one part where most leave two. A part
-    // costs about as much as kPartBlocks blocks (its stores, and the merge of it).
-    // Measured: 43.0 us a pass divided evenly and 38.7 by unit at T=61 B=4 C=4096,
-    // 87.3 and 88.0 at T=256 C=16384.
+    // fewer CTAs may work, but each leaves one part where most leave two; or among a
+    // cluster, whose CTAs merge their parts in shared memory. A part that goes through
+    // memory costs about as much as kPartBlocks blocks (its stores, and the merge of it).
+    // Measured, evenly, by unit, by clusters: 43.0, 36.4 and 31.6 us a pass at T=61 B=4
+    // C=4096; 85.3, 88.0 and 81.7 at T=256 C=16384.
     constexpr int kPartBlocks = 2;
-    const int units = (int)(total / p.nb), k = std::min(a.num_sms / units, p.nb);
-    const int even = (int)((total + a.num_sms - 1) / a.num_sms) + 2 * kPartBlocks;
-    const bool by_unit = k >= 1 && (p.nb + k - 1) / k + kPartBlocks <= even;
+    const int units = (int)(total / p.nb), most = std::min(a.num_sms / units, p.nb);
+    int k = 0, cost = (int)((total + a.num_sms - 1) / a.num_sms) + 2 * kPartBlocks;  // 0: evenly
+    if (most >= 1 && (p.nb + most - 1) / most + kPartBlocks <= cost) {
+        k = most;
+        cost = (p.nb + most - 1) / most + kPartBlocks * (most > 1);
+    }
+    p.cluster = 0;
+    for (int c = std::min(most, kMaxCluster); c > 1 && (p.nb + c - 1) / c <= cost; --c) {
+        int fit = 0;  // all at once, or the last clusters would wait for the first
+        if (cudaError_t e = clusters_at_once<D>(c, &fit); e != cudaSuccess) return e;
+        if (units > fit) continue;
+        k = p.cluster = c;
+        break;
+    }
+    const bool by_unit = k > 0;
     const int ctas = by_unit ? units * k : (int)std::min<long long>(a.num_sms, total);
     p.split.run = by_unit ? p.nb : (int)total;
     p.split.k = by_unit ? k : ctas;
@@ -700,7 +827,23 @@ cudaError_t tree_launch(const TreeArgs& a) {
     // Up to kMergeRows rows per KV head are merged by the unit's last CTA: measured,
     // one token over 2048 slots, 14.4 us a pass against 15.4 with a kernel.
     constexpr int kMergeRows = 32;
-    p.count = by_unit && R <= kMergeRows ? a.count : nullptr;
+    p.count = by_unit && R <= kMergeRows && !p.cluster ? a.count : nullptr;
+    if (p.cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(Cfg::THREADS);
+        cfg.dynamicSmemBytes = Cfg::SMEM;
+        cfg.stream = a.stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = k;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D>, mq, mkc, mvc, mk, mv, p);
+    }
     cudaError_t e = launch_ex(true, tree_tc_kernel<D>, dim3(ctas), dim3(Cfg::THREADS), Cfg::SMEM, a.stream, mq, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;
     bool divided = false;
