@@ -152,7 +152,8 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     a.wb.ns = c->wait_ns;
     a.stream = (cudaStream_t)stream;
     a.num_sms = c->num_sms;
-    const bool tc = c->use_tc && (long long)c->B * c->Hq * T * (c->n + T) * c->d > kTreeSimtProducts;
+    const long long simt = c->Hq / c->Hkv * T <= kTreeFewRows ? kTreeSimtProductsFew : kTreeSimtProducts;
+    const bool tc = c->use_tc && (long long)c->B * c->Hq * T * (c->n + T) * c->d > simt;
     H2O_TRY(c, tc ? launch_tree_tc(a) : launch_tree_simt(a), "launch tree attention");
     return H2O_OK;
 } catch (const std::exception& e) {

@@ -39,10 +39,13 @@ cudaError_t launch_tree_tc(const TreeArgs& a);  // bf16
 size_t tree_part_floats(int num_sms, int d);
 size_t tree_simt_part_floats(int num_sms, int d);
 // bf16: up to so many products of a query and a key channel take the CUDA cores, where
-// the tensor-core kernel's way through TMEM costs more than the arithmetic. Measured,
-// us on the device, CUDA cores / tensor cores: 0.05 million 5.6 / 8.8, 0.7 million
-// 6.1 / 8.6, 8.4 million 10.9 / 12.7, 16.8 million 15.0 / 12.6, 67 million 34.4 / 24.5.
-constexpr long long kTreeSimtProducts = 10ll << 20;
+// the tensor-core kernel's way through TMEM costs more than the arithmetic; more where a
+// KV head has few rows, which read each key once or twice. Measured, us a pass, CUDA
+// cores / tensor cores, millions of products: 4 or 8 rows: 8.4: 8.0 / 11.9, 16.8:
+// 11.1 / 12.0, 30.7: 15.1 / 15.9, 33.6: 16.8 / 15.8; 12 to 64 rows: 3.8: 6.6 / 7.8, 8.5:
+// 9.9 / 9.6 (d = 64: 11.6 / 8.1), 16.8: 12.3 / 10.5.
+constexpr int kTreeFewRows = 8;
+constexpr long long kTreeSimtProductsFew = 30ll << 20, kTreeSimtProducts = 8ll << 20;
 
 // 8-bit record of a step's inputs: codes of q, k, v (the chunk) and of the n
 // valid slots of K and V, row after row, then their scales in the same order.

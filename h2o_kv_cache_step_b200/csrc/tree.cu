@@ -25,14 +25,15 @@ constexpr int kTreeMinKeys = 96;  // keys that repay a CTA of their own
 // One CTA per kRows query rows of one KV group (row = head-in-group * T + i), four
 // where that still gives every SM a CTA (each key is then read once for four rows),
 // one otherwise (latency: 6.2 us against 10.1 at 24 nodes, 201 slots, 4 / 2
-// heads). Eight lanes share a key (d / 8 columns each), so a warp takes four keys and
+// heads; 5.1 since four keys per lane group are in flight). Eight lanes share a key (d / 8 columns each), so a warp takes four keys and
 // the CTA 32 at a time, straight from global memory into registers; every lane
 // group keeps its own running maximum, sum and output, merged at the end.
 // Where the rows are few (`slice` < n + T) the keys are divided among CTAs, `slice`
 // each: a CTA leaves its unnormalised rows, maxima (NaN: the node is absent) and
 // sums, and the last one of its rows to arrive merges them, in order. One token over
 // 2048 slots is bound by latency: the loads, two exchanges through shared memory and
-// the merge's way through L2 (10.9 us on the device, 12.7 on the tensor cores).
+// the merge's way through L2 (8.2 us on the device, 10.5 with the loads of two keys in
+// flight per lane group instead of four; 11.9 a pass on the tensor cores, 8.0 here).
 struct TreeSplit {
     int slice;        // keys per CTA, a multiple of 32
     int parts;        // CTAs per kRows rows

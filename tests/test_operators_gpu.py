@@ -80,6 +80,11 @@ TREES = [
     (BF16, 8, 8, 3, 128, 300, 0, 77),
     (BF16, 16, 4, 1, 128, 40, 33, 256),
     (BF16, 2, 4, 1, 128, 16384, 16383, 5),
+    (BF16, 8, 8, 4, 128, 1100, 1097, 1),  # few rows of many sequences
+    (BF16, 16, 8, 1, 128, 2100, 2051, 1),
+    (BF16, 16, 8, 2, 64, 900, 897, 3),
+    (BF16, 1, 8, 4, 128, 9000, 8999, 1),  # one sequence, its keys divided among many CTAs
+    (BF16, 14, 8, 4, 128, 2100, 2065, 40),  # more units than a CTA each
     (FP32, 1, 1, 2, 64, 3000, 2990, 1),   # fp32, the keys divided
     (FP32, 1, 2, 4, 128, 900, 899, 2),
 ]
