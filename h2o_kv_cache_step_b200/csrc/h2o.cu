@@ -582,15 +582,6 @@ int h2o_set_policy(h2o_ctx* c, int policy) {
                             cudaGetErrorString(e));
             }
         }
-        // the last key block of a partly filled compact cache reads rows that nothing
-        // has written yet: weight 0 times what the memory held before must not be NaN
-        cudaError_t e = cudaMemset(bufs[0], 0, bytes[0]);
-        if (e == cudaSuccess) e = cudaMemset(bufs[1], 0, bytes[1]);
-        if (e == cudaSuccess) e = cudaDeviceSynchronize();
-        if (e != cudaSuccess) {
-            for (void* p : bufs) cudaFree(p);
-            return cuda_fail(c, e, "clearing the insert-always workspace");
-        }
         c->ins_K = bufs[0];
         c->ins_V = bufs[1];
         c->ins_slot = static_cast<int32_t*>(bufs[2]);

@@ -19,6 +19,8 @@
 // sums of the chunk path write the new scores and positions into the slot
 // layout (insert_finish_kernel); the chunk path's copy kernel then writes the
 // chunk's K and V into their slots.
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace h2o {
@@ -180,22 +182,32 @@ insert_select_kernel(const float* __restrict__ scores, const int32_t* __restrict
     for (int c = threadIdx.x; c < tot_k + T; c += blockDim.x) ko[c] = 1;
 }
 
-// One warp per compact entry r: copies the K and V rows of its slot.
+// One warp per row r of the compact cache up to the end of the last 128-row key block
+// that the attention loads (at most C rows): a kept entry's K and V rows are copied from
+// its slot, rows past the n_kept entries are zeroed. They hold what an earlier, longer
+// set of entries left there, of another sequence perhaps, and weight zero times a NaN
+// is not zero.
+constexpr int kKeyBlock = 128;
+
 __global__ void __launch_bounds__(256)
 gather_kernel(const uint4* __restrict__ Kc, const uint4* __restrict__ Vc, uint4* __restrict__ Kq,
-              uint4* __restrict__ Vq, const int32_t* __restrict__ compact_slot, int C, int n_kept,
+              uint4* __restrict__ Vq, const int32_t* __restrict__ compact_slot, int C, int n_kept, int rows,
               int row_vecs) {
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = blockIdx.x * 8 + warp;
     const size_t bg = blockIdx.y;
-    if (r >= n_kept) return;
+    if (r >= rows) return;
+    uint4* kd = Kq + (bg * C + r) * (size_t)row_vecs;
+    uint4* vd = Vq + (bg * C + r) * (size_t)row_vecs;
+    if (r >= n_kept) {
+        for (int e = lane; e < row_vecs; e += 32) kd[e] = vd[e] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const int j = compact_slot[bg * (size_t)C + r];
     const uint4* ks = Kc + (bg * C + j) * (size_t)row_vecs;
     const uint4* vs = Vc + (bg * C + j) * (size_t)row_vecs;
-    uint4* kd = Kq + (bg * C + r) * (size_t)row_vecs;
-    uint4* vd = Vq + (bg * C + r) * (size_t)row_vecs;
     for (int e = lane; e < row_vecs; e += 32) {
         kd[e] = ks[e];
         vd[e] = vs[e];
@@ -258,9 +270,10 @@ cudaError_t launch_gather(const StepArgs& a, int n_kept) {
     if (n_kept == 0) return cudaSuccess;
     const int elem = a.dtype == 1 ? 4 : 2;
     const int row_vecs = a.d * elem / 16;
-    cudaError_t e = launch_ex(true, gather_kernel, dim3((n_kept + 7) / 8, a.B * a.Hkv), dim3(256), 0, a.stream,
+    const int rows = std::min(a.C, (n_kept + kKeyBlock - 1) / kKeyBlock * kKeyBlock);
+    cudaError_t e = launch_ex(true, gather_kernel, dim3((rows + 7) / 8, a.B * a.Hkv), dim3(256), 0, a.stream,
                               (const uint4*)a.Kc, (const uint4*)a.Vc, (uint4*)a.ins_K, (uint4*)a.ins_V,
-                              (const int32_t*)a.ins_slot, a.C, n_kept, row_vecs);
+                              (const int32_t*)a.ins_slot, a.C, n_kept, rows, row_vecs);
     if (e != cudaSuccess) return e;
     a.log->done("gather_kernel", a.stream);
     return cudaGetLastError();

@@ -371,3 +371,39 @@ def test_full_size_sampled(name, policy):
     compare_scores(g["cand_score"][b, gg], res.cand_score[0, 0, :nc], f"{name} group scores")
     assert np.abs(g["out"][b, gg * G:(gg + 1) * G] - res.out[0]).max() <= TOL_OUT["bf16"]
     check_selection_replay(g, pre, k, v, wl.C, T, policy)
+
+
+@pytest.mark.parametrize("again", ["reset", "set_state"])
+@pytest.mark.parametrize("dtype,Hkv,G,d,C,T", [("bf16", 2, 4, 128, 256, 100), ("bf16", 3, 2, 64, 200, 60),
+                                               ("bf16", 2, 4, 128, 90, 4), ("fp32", 2, 2, 64, 130, 33)])
+def test_insert_always_forgets_the_sequence_before(dtype, Hkv, G, d, C, T, again):
+    """A sequence whose v holds NaNs, then a clean one on the same context, which
+    starts from an empty cache or from a restored one: what a new context computes,
+    bit for bit. The clean one's last key block ends among rows that the other filled."""
+    from h2o_kv_cache_step_b200._lib import H2O_POLICY_INSERT_ALWAYS
+    gen = torch.Generator(device="cuda").manual_seed(C + T)
+
+    def chunk():
+        return [torch.randn((1, h, T, d), generator=gen, device="cuda").to(TORCH_DTYPE[dtype]) for h in (Hkv * G, Hkv, Hkv)]
+
+    def new():
+        cache = H2OCache(1, Hkv * G, Hkv, d, C, TORCH_DTYPE[dtype], max_T=T)
+        cache.set_policy(H2O_POLICY_INSERT_ALWAYS)
+        return cache
+
+    used, fresh = new(), new()
+    for _ in range(C // T + 2):
+        q, k, v = chunk()
+        used.step(q, k, torch.full_like(v, float("nan")))
+    clean = [chunk() for _ in range(3)]
+    fresh.step(*clean[0])
+    if again == "set_state":
+        state = fresh.get_state()
+        used.set_state(*state)
+    else:
+        used.reset()
+        used.step(*clean[0])
+    for x in clean[1:]:
+        assert torch.equal(used.step(*x), fresh.step(*x))
+    for a, b in zip(used.get_state(), fresh.get_state()):
+        assert torch.equal(a, b) if torch.is_tensor(a) else a == b
