@@ -103,7 +103,11 @@ inline int fail(h2o_ctx* c, int code, const char* fmt, ...) {
     return code;
 }
 
+// The status reports the error, so the runtime's own record of it goes: the launchers
+// end in cudaGetLastError(), and the next call of this thread would fail with an
+// allocation that this one could not make. (What breaks the CUDA context stays.)
 inline int cuda_fail(h2o_ctx* c, cudaError_t e, const char* what) {
+    cudaGetLastError();
     return fail(c, e == cudaErrorMemoryAllocation ? H2O_ERR_OOM : H2O_ERR_CUDA, "%s: %s (%s)", what,
                 cudaGetErrorString(e), cudaGetErrorName(e));
 }

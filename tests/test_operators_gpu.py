@@ -652,3 +652,18 @@ def test_refusals():
     with pytest.raises(H2OError, match="insert-always"):
         c.checkpoint(q, k, v)
     c.sync_check()
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_a_failed_allocation_leaves_the_next_step_alone(dtype):
+    """A backward whose workspace fits no card (it fails before anything is launched
+    or read) and then a step."""
+    q, k, v, K, V = heads(dtype, 1, 1, 2, 128, 64, 50, 40)
+    c, other = cache_of(K, V, 2, 50), cache_of(K, V, 2, 50)
+    p = q.data_ptr()
+    rc = _lib.lib().h2o_checkpoint_backward(c.handle, p, 2**62, 2**29, 50, p, p, p, p, p, p, None)
+    assert rc == _lib.H2O_ERR_OOM
+    assert torch.equal(c.step(q, k, v), other.step(q, k, v))
+    ck, dout = c.checkpoint(q, k, v), torch.randn_like(q)
+    for a, b in zip(c.checkpoint_backward(ck, dout), other.checkpoint_backward(ck, dout)):
+        assert torch.equal(a, b)
