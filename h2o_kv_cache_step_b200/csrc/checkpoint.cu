@@ -17,7 +17,9 @@
 //   or a's significand (then that is 127 times a power of two, and 127 / a is
 //   exact). With 127 / a taken two units too large, the first lands just above 63.5
 //   and goes to 64, the even one; the second takes the exact power of two. One
-//   multiply-add and its rounding give the code.
+//   multiply-add and its rounding give the code. Groups near the ends of fp32's range
+//   are moved by a power of two, which leaves quotients alone: 1 / a has to be a normal
+//   number, or it is off by more than the two units.
 //   fp32, in 64 bits: the remainder 127 x - code a is exact, is +-a / 2 on a
 //   border, and an odd code then moves to its even neighbour.
 //
@@ -127,10 +129,11 @@ __device__ __forceinline__ void store16(__nv_bfloat16* x, const float (&f)[kPer]
 // in the low bytes of c. Adding 1.5 * 2^23 rounds to a whole number, ties to
 // even, and leaves it in the low bits.
 __device__ __forceinline__ void codes16(float (&f)[kPer], float a, uint32_t (&c)[kPer], __nv_bfloat16) {
-    if (a < 0x1p-100f) {  // 127 / a stays in range
-        a *= 0x1p60f;
+    if (a < 0x1p-100f || a >= 0x1p100f) {  // 127 / a stays in range, 1 / a normal (24 bits)
+        const float by = a < 1.f ? 0x1p60f : 0x1p-60f;
+        a *= by;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] *= 0x1p60f;
+        for (int i = 0; i < kPer; ++i) f[i] *= by;
     }
     const uint32_t bits = __float_as_uint(a);
     const float over = __uint_as_float(__float_as_uint(127.f * __frcp_rn(a)) + 2);

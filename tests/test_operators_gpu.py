@@ -667,3 +667,9 @@ def test_a_failed_allocation_leaves_the_next_step_alone(dtype):
     ck, dout = c.checkpoint(q, k, v), torch.randn_like(q)
     for a, b in zip(c.checkpoint_backward(ck, dout), other.checkpoint_backward(ck, dout)):
         assert torch.equal(a, b)
+
+
+def test_checkpoint_codes_of_the_largest_bf16_quotients():
+    """As above up to the type's largest value: magnitudes whose reciprocals are subnormal."""
+    for exponent in (118, 119, 120):
+        test_checkpoint_codes_of_every_bf16_quotient(exponent)
