@@ -2,7 +2,8 @@
 // carried through the eviction.
 //
 // Record: with a = max |x| over 32 consecutive channels of a row,
-//   code = rint(127 x / a) (ties to even), scale = a / 127 rounded to fp32,
+//   code = rint(127 x / a) (ties to even), scale = a / 127 rounded to fp32 (down for
+//   fp32's largest value, whose 127 scale would round to infinity),
 // and the value it stands for is code * scale, rounded to the element type. A
 // group of zeros has scale 0; a group with a NaN or an infinity has scale NaN
 // and stands for NaNs.
@@ -41,6 +42,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 16;  // values per thread at a time; two threads share a group of 32
 constexpr int kSaveIter = 2, kRestoreIter = 1;  // times
 static_assert(kCkptGroup == 2 * kPer, "a group is a pair of threads");
+constexpr float kMaxScale = 0x1.020406p+121f;  // 127 times the next value is infinite in fp32
 
 // The five sections of a record (q, k, v, K, V): `outer` runs of `rows` rows in
 // the record, and of `pitch` rows in the tensors (rows past `rows` are empty).
@@ -187,7 +189,8 @@ ckpt_save_kernel(const __grid_constant__ Sections sec, int8_t* __restrict__ code
         const unsigned long long at = (p.code + it * kRows<D>) * D + p.col;
         *reinterpret_cast<uint4*>(codes + at) = make_uint4(w[0], w[1], w[2], w[3]);
         if (p.col % kCkptGroup == 0)
-            scales[at / kCkptGroup] = coded || top == 0 ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
+            scales[at / kCkptGroup] =
+                coded || top == 0 ? fminf(__fdiv_rn(a, 127.f), kMaxScale) : __uint_as_float(0x7fffffffu);
     }
 }
 

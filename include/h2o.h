@@ -257,11 +257,13 @@ int h2o_checkpoint_bytes(const h2o_ctx *ctx, int T, int n, size_t *bytes);
  *   float  scales: the same order, [.., d / H2O_CKPT_GROUP].
  * With a = max |x| over a group of H2O_CKPT_GROUP channels, a code is
  * 127 x / a rounded to the nearest whole number (ties to even) and the scale
- * a / 127; the value they stand for is code * scale rounded to the element
- * type, off by at most a / 254 and that rounding. A group of zeros has scale 0;
- * a group with a NaN or an infinity stands for NaNs. H2O_ERR_UNSUPPORTED under
- * H2O_POLICY_INSERT_ALWAYS, whose steps do not attend to the cache they start
- * from. Asynchronous on `stream`; no allocation. */
+ * a / 127 rounded to float (down where 127 times it would be infinite); the
+ * value they stand for is code * scale rounded to the element type, finite and
+ * off by at most a / 254 and those roundings (that of a subnormal scale, below
+ * a = 2^-119, counts 127 times: tiny groups keep fewer bits). A group of zeros
+ * has scale 0; a group with a NaN or an infinity stands for NaNs.
+ * H2O_ERR_UNSUPPORTED under H2O_POLICY_INSERT_ALWAYS, whose steps do not attend
+ * to the cache they start from. Asynchronous on `stream`; no allocation. */
 int h2o_checkpoint_save(h2o_ctx *ctx, const void *q, const void *k, const void *v, int T,
                         void *ckpt, size_t bytes, void *stream);
 

@@ -673,3 +673,25 @@ def test_checkpoint_codes_of_the_largest_bf16_quotients():
     """As above up to the type's largest value: magnitudes whose reciprocals are subnormal."""
     for exponent in (118, 119, 120):
         test_checkpoint_codes_of_every_bf16_quotient(exponent)
+
+
+def test_checkpoint_values_over_the_whole_range_of_fp32():
+    """Every power of two and the values next to it, the largest finite one among them:
+    finite, and off by at most half a code, the scale's rounding and the product's."""
+    e = torch.arange(-149, 128, dtype=torch.float64)
+    tops = torch.cat([2.0**e, 1.5 * 2.0**e[1:], (2 - 2.0**-23) * 2.0**e[23:]])
+    gen = torch.Generator().manual_seed(1)
+    x = tops[:, None] * torch.cat([torch.ones(len(tops), 1, dtype=torch.float64),
+                                   2 * torch.rand((len(tops), 31), generator=gen, dtype=torch.float64) - 1], 1)
+    x = torch.cat([x, -x]).float()
+    rows = torch.cat([x, x.new_zeros((-len(x) % 2, 32))]).view(1, 1, -1, 64).cuda()
+    c = H2OCache(1, 1, 1, 64, 4, FP32, max_T=rows.shape[2])
+    back = c.checkpoint_restore(c.checkpoint(rows, rows, -rows))
+    for got, want in zip(back, (rows, rows, -rows)):
+        assert got.isfinite().all()
+        w = want.double().unflatten(-1, (-1, 32))
+        top = w.abs().amax(-1, keepdim=True)
+        # a / 254, and twice the roundings (2^-24, or half the smallest step): the scale's,
+        # 127 times where it is subnormal, and the product's
+        bound = top / 254 + 2 * (2 * ref.U32 * top + 128 * 2.0**-150)
+        assert ((got.double().unflatten(-1, (-1, 32)) - w).abs() <= bound).all()
