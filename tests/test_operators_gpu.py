@@ -695,3 +695,40 @@ def test_checkpoint_values_over_the_whole_range_of_fp32():
         # 127 times where it is subnormal, and the product's
         bound = top / 254 + 2 * (2 * ref.U32 * top + 128 * 2.0**-150)
         assert ((got.double().unflatten(-1, (-1, 32)) - w).abs() <= bound).all()
+
+
+LARGE_BACKWARDS = [
+    # dtype, B, Hkv, G, d, C, n, T: grids of several waves on the tensor cores, query tiles that
+    # hold the end of one head and the start of another
+    (BF16, 1, 8, 4, 128, 2048, 2048, 1024),
+    (BF16, 4, 8, 3, 64, 1500, 1409, 333),
+    (BF16, 2, 8, 5, 128, 1100, 1037, 260),
+    # fp32: two query rows per CTA and one key, then two of both
+    (FP32, 2, 2, 2, 64, 70, 61, 77),
+    (FP32, 1, 2, 4, 128, 300, 257, 151),
+    (FP32, 3, 2, 1, 64, 200, 200, 101),
+]
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,C,n,T", LARGE_BACKWARDS)
+def test_large_backward_from_a_checkpoint(dtype, B, Hkv, G, d, C, n, T):
+    """As above, the 64-bit definition one KV head at a time."""
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, C, n, T, seed=n + T)
+    c = cache_of(K, V, Hkv * G, n)
+    ck = c.checkpoint(q, k, v)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(dtype)
+    rest = c.checkpoint_restore(ck)
+    got = c.checkpoint_backward(ck, dout)
+    c.sync_check()
+    assert not got[1][:, :, n:].any() and not got[2][:, :, n:].any()
+    for b in range(B):
+        for g in range(Hkv):
+            def one(x):
+                per = x.shape[1] // Hkv
+                return x[b:b + 1, g * per:(g + 1) * per]
+            want, bound = ref.backward(*map(one, rest), one(dout), n, dtype)
+            for name, x, w, lim in zip(("dq", "dK", "dV", "dk", "dv"), got, want, bound):
+                x = one(x)
+                ref.within((name, b, g), x[:, :, :n] if name in ("dK", "dV") else x, w, lim)
+    for a, b in zip(got, c.checkpoint_backward(ck, dout)):
+        assert torch.equal(a, b)
