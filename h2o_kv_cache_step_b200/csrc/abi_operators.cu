@@ -28,15 +28,23 @@ bool capturing(cudaStream_t s) {
 // Counters at the start of the checkpoint workspace, one per SM, zero between calls.
 size_t ckpt_count_bytes(const h2o_ctx* c) { return (sizeof(unsigned) * c->num_sms + 255) & ~(size_t)255; }
 
-// The checkpoint workspace, at least `bytes` large.
+// The checkpoint workspace, at least `bytes` large. An outgrown one is replaced by one
+// of twice its size, if the card has that much, so that calls that grow step by step
+// allocate rarely and what is kept of them is less than the one in use.
 int checkpoint_workspace(h2o_ctx* c, size_t bytes, cudaStream_t s) {
     if (bytes <= c->ckpt_ws_bytes) return H2O_OK;
     if (capturing(s))
         return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
     c->retired.reserve(c->retired.size() + 1);
     void* p = nullptr;
-    H2O_TRY(c, cudaMalloc(&p, bytes), "cudaMalloc(checkpoint workspace)");
-    cudaError_t e = cudaMemset(p, 0, ckpt_count_bytes(c));
+    size_t got = std::max(bytes, 2 * c->ckpt_ws_bytes);
+    cudaError_t e = cudaMalloc(&p, got);
+    if (e == cudaErrorMemoryAllocation && got > bytes) {
+        cudaGetLastError();
+        e = cudaMalloc(&p, got = bytes);
+    }
+    if (e != cudaSuccess) return cuda_fail(c, e, "cudaMalloc(checkpoint workspace)");
+    e = cudaMemset(p, 0, ckpt_count_bytes(c));
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaFree(p);
@@ -44,7 +52,7 @@ int checkpoint_workspace(h2o_ctx* c, size_t bytes, cudaStream_t s) {
     }
     if (c->ckpt_ws) c->retired.push_back(c->ckpt_ws);  // room reserved above
     c->ckpt_ws = p;
-    c->ckpt_ws_bytes = bytes;
+    c->ckpt_ws_bytes = got;
     return H2O_OK;
 }
 

@@ -732,3 +732,23 @@ def test_large_backward_from_a_checkpoint(dtype, B, Hkv, G, d, C, n, T):
                 ref.within((name, b, g), x[:, :, :n] if name in ("dK", "dV") else x, w, lim)
     for a, b in zip(got, c.checkpoint_backward(ck, dout)):
         assert torch.equal(a, b)
+
+
+def test_backwards_of_growing_chunks_keep_few_workspaces():
+    """Chunks that grow by a little past the context's length: outgrown workspaces stay
+    (a graph may hold them), all of them together no more than the one in use."""
+    B, Hq, C, d, last = 1, 32, 16, 128, 1280
+    c = H2OCache(B, Hq, 1, d, C, FP32, max_T=4)
+    flat = [torch.zeros((B, h, last, d), device="cuda") for h in (Hq, 1, 1, Hq, Hq, 1, 1)]
+    dK, dV = torch.zeros((B, 1, C, d), device="cuda"), torch.zeros((B, 1, C, d), device="cuda")
+    record = torch.zeros(B * (Hq + 2) * last * (d + d // 8), dtype=torch.uint8, device="cuda")
+    P = [x.data_ptr() for x in flat]
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for T in range(320, last + 1, 16):
+        c._check(_lib.lib().h2o_checkpoint_backward(c.handle, record.data_ptr(), record.numel(), T, 0, P[3], P[4],
+                                                    dK.data_ptr(), dV.data_ptr(), P[5], P[6], None))
+    c.sync_check()
+    largest = 4 * B * (Hq + 2) * last * d + 16 * B * Hq * last + (32 << 20)  # the step, its statistics, parts and pages
+    # grown to twice its size when outgrown: at most 2 + 1 + 1/2 + ... of the last one needed
+    assert free - torch.cuda.mem_get_info()[0] <= 4 * largest
