@@ -51,13 +51,17 @@ def stale() -> bool:
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """``_torch_ops.so``, linked to the library beside it and to torch's own."""
-    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "h2o.h"), __file__))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+    """``_torch_ops.so``, linked to the library beside it and to torch's own; built
+    anew for another torch or Python too, whose object layouts it uses."""
     import sysconfig
 
     import torch
+    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "h2o.h"), __file__))
+    built_for = f"torch {torch.__version__} in {os.path.dirname(torch.__file__)}, Python {sys.version}"
+    stamp = os.path.join(BUILD, "torch_ops.stamp")
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
+            and os.path.exists(stamp) and open(stamp).read() == built_for):
+        return BINDING
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + f".tmp{os.getpid()}"
@@ -73,6 +77,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("build of _torch_ops.so failed")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

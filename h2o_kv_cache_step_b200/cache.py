@@ -7,6 +7,7 @@ every computation happens in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -26,6 +27,8 @@ def _ops_type():
     lib()
     try:
         from . import _torch_ops
+        if torch.__version__.split("+")[0] != _torch_ops.torch_version:
+            raise ImportError(f"built with torch {_torch_ops.torch_version}, this is {torch.__version__}")
     except ImportError as e:
         raise ImportError(f"_torch_ops.so is missing or does not load ({e}): build it with "
                           "`python -m h2o_kv_cache_step_b200.build`") from e
@@ -101,7 +104,12 @@ class H2OCache:
         rc = lib().h2o_create_ex(B, Hq, Hkv, d, C, _DTYPES[dtype], int(max_T or C), ctypes.byref(h))
         check(rc, None)
         self._h = h
-        self._ops = self._bind(h.value)
+
+    @functools.cached_property
+    def _ops(self):
+        """The operators' binding, loaded by the first call of one: the step and the
+        rest need the library alone."""
+        return self._bind(self._h.value if self._h else 0)
 
     def _bind(self, handle: int):
         return _ops_type()(handle, self.device.index, self.B, self.Hq, self.Hkv, self.d, self.C, self.dtype == torch.bfloat16)
@@ -111,7 +119,7 @@ class H2OCache:
         if getattr(self, "_h", None):
             lib().h2o_destroy(self._h)
             self._h = None
-            self._ops = self._bind(0)  # refuses further calls
+            self.__dict__.pop("_ops", None)  # bound anew, to no context, by a further call
 
     def __del__(self):
         try:

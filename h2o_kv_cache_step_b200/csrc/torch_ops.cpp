@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <array>
 #include <string>
@@ -254,6 +255,11 @@ PyMODINIT_FUNC PyInit__torch_ops() {
     if (PyType_Ready(&ops_type) < 0) return nullptr;
     PyObject* m = PyModule_Create(&module);
     if (!m) return nullptr;
+    // the tensors' layout is that of the torch this was compiled with
+    if (PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
     Py_INCREF(&ops_type);
     if (PyModule_AddObject(m, "Ops", reinterpret_cast<PyObject*>(&ops_type)) < 0) {
         Py_DECREF(&ops_type);

@@ -117,3 +117,51 @@ def test_reference_backward_against_differences():
             lo[i][at] -= 1e-5
             hi[i][at] += 1e-5
             assert abs((loss(*hi) - loss(*lo)) / 2e-5 - float(g[at])) < 1e-6
+
+
+class _FakeLibrary:
+    """Contexts without a device (and without an address: nothing to destroy)."""
+    def h2o_create_ex(self, *args):
+        return 0
+
+
+def test_a_cache_needs_the_operators_module_only_for_the_operators(monkeypatch):
+    """A library without the torch module beside it still makes caches and steps."""
+    from h2o_kv_cache_step_b200 import cache
+
+    def missing():
+        raise ImportError("_torch_ops.so is missing")
+
+    monkeypatch.setattr(cache, "lib", _FakeLibrary)
+    monkeypatch.setattr(cache, "_ops_type", missing)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    c = H2OCache(2, 4, 2, 64, 32)
+    x = _t(2, 4, 5, 64)
+    with pytest.raises(ValueError, match="q: need contiguous CUDA"):
+        c.step(x, x, x)
+    with pytest.raises(ImportError, match="_torch_ops.so is missing"):
+        c.tree_attend(x, x, x, x)
+
+
+def test_a_module_of_another_torch_is_refused(L, monkeypatch):
+    from h2o_kv_cache_step_b200 import cache
+    cache._ops_type()
+    monkeypatch.setattr(torch, "__version__", "1.0.0+cu1")
+    with pytest.raises(ImportError, match="built with torch .* this is 1.0.0.*build it with"):
+        cache._ops_type()
+
+
+def test_the_operators_module_is_built_anew_for_another_torch(L, monkeypatch):
+    import subprocess
+
+    from h2o_kv_cache_step_b200 import build
+
+    def compiler(cmd, **kw):
+        raise RuntimeError("compiled")
+
+    build.build_binding()
+    monkeypatch.setattr(subprocess, "run", compiler)
+    build.build_binding()  # up to date
+    monkeypatch.setattr(torch, "__version__", "1.0.0+cu1")
+    with pytest.raises(RuntimeError, match="compiled"):
+        build.build_binding()
