@@ -7,6 +7,7 @@
 // graph may hold its address.
 #include <algorithm>
 #include <exception>
+#include <mutex>
 
 #include "context.h"
 #include "operators.h"
@@ -119,6 +120,7 @@ int h2o_tree_attend(h2o_ctx* c, const void* q, const void* k, const void* v, con
     if ((reinterpret_cast<uintptr_t>(parent) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3))
         return fail(c, H2O_ERR_ALIGN, "parent and lse must be 4-byte aligned");
     DeviceGuard g(c->device);
+    const std::lock_guard<std::mutex> lock(c->workspaces);
     if (!c->tree_part) {
         if (capturing((cudaStream_t)stream))
             return fail(c, H2O_ERR_UNSUPPORTED, "the workspace has to be allocated outside a capture: make the call once before");
@@ -260,6 +262,7 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
     };
     const size_t oq = take(nq * c->elem), ok = take(nk * c->elem), ov = take(nk * c->elem);
     const size_t oK = take(nK * c->elem), oV = take(nK * c->elem), os = take(sizeof(float) * ckpt_stats_floats(most));
+    const std::lock_guard<std::mutex> lock(c->workspaces);
     rc = checkpoint_workspace(c, end, s);
     if (rc != H2O_OK) return rc;
     char* w = static_cast<char*>(c->ckpt_ws);

@@ -6,6 +6,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 #include <vector>
 
 #include "../../include/h2o.h"
@@ -79,6 +80,7 @@ struct h2o_ctx {
     void* ckpt_ws = nullptr;
     size_t ckpt_ws_bytes = 0;
     std::vector<void*> retired;
+    std::mutex workspaces;  // held by the calls that use them: two threads' calls are queued one after the other
     // per-kernel profiling
     bool prof_on = false;
     int prof_max_steps = 0, prof_steps = 0;

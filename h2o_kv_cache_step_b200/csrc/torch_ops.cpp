@@ -68,6 +68,24 @@ at::Tensor make(const Ops* s, at::ScalarType dtype, at::IntArrayRef shape) {
 
 void* stream(const Ops* s) { return c10::cuda::getCurrentCUDAStream(s->device).stream(); }
 
+// Python's other threads run during a call of the library, which may wait for the GPU
+// (a context's first call of an operator allocates).
+class Unlocked {
+    PyThreadState* const state_ = PyEval_SaveThread();
+
+public:
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
+template <typename F>
+int unlocked(F&& call) {
+    const Unlocked u;
+    return call();
+}
+
 int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw PythonError();
@@ -116,8 +134,11 @@ PyObject* tree_attend(const Ops* s, PyObject* const* a, Py_ssize_t n) {
     const void *q = need(s, "q", a[0], s->dtype, rows), *k = need(s, "k", a[1], s->dtype, chunk);
     const void *v = need(s, "v", a[2], s->dtype, chunk), *parent = need(s, "parent", a[3], at::kInt, tree);
     at::Tensor out = make(s, s->dtype, rows), lse = make(s, at::kFloat, at::IntArrayRef(rows.data(), 3));
-    const int rc = h2o_tree_attend(s->ctx, q, k, v, static_cast<const int32_t*>(parent), out.data_ptr(),
-                                   static_cast<float*>(lse.data_ptr()), narrow("q", T), stream(s));
+    const int t = narrow("q", T);
+    const int rc = unlocked([&] {
+        return h2o_tree_attend(s->ctx, q, k, v, static_cast<const int32_t*>(parent), out.data_ptr(),
+                               static_cast<float*>(lse.data_ptr()), t, stream(s));
+    });
     return result(rc, std::move(out), std::move(lse));
 }
 
@@ -134,7 +155,7 @@ PyObject* checkpoint(const Ops* s, PyObject* const* a, Py_ssize_t nargs) {
     if (rc == H2O_OK) rc = h2o_checkpoint_bytes(s->ctx, narrow("q", T), (int)n, &bytes);
     if (rc != H2O_OK) return PyLong_FromLong(rc);
     at::Tensor buf = make(s, at::kByte, {(int64_t)bytes});
-    rc = h2o_checkpoint_save(s->ctx, q, k, v, (int)T, buf.data_ptr(), bytes, stream(s));
+    rc = unlocked([&] { return h2o_checkpoint_save(s->ctx, q, k, v, (int)T, buf.data_ptr(), bytes, stream(s)); });
     if (rc != H2O_OK) return PyLong_FromLong(rc);
     return Py_BuildValue("(NL)", THPVariable_Wrap(std::move(buf)), (long long)n);
 }
@@ -163,8 +184,10 @@ PyObject* checkpoint_restore(const Ops* s, PyObject* const* a, Py_ssize_t n) {
     const Shape rows{s->B, s->Hq, r.T, s->d}, chunk{s->B, s->Hkv, r.T, s->d}, cache{s->B, s->Hkv, s->C, s->d};
     at::Tensor q = make(s, s->dtype, rows), k = make(s, s->dtype, chunk), v = make(s, s->dtype, chunk);
     at::Tensor K = make(s, s->dtype, cache), V = make(s, s->dtype, cache);
-    const int rc = h2o_checkpoint_restore(s->ctx, r.p, r.bytes, r.T, r.n, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                          K.data_ptr(), V.data_ptr(), stream(s));
+    const int rc = unlocked([&] {
+        return h2o_checkpoint_restore(s->ctx, r.p, r.bytes, r.T, r.n, q.data_ptr(), k.data_ptr(), v.data_ptr(), K.data_ptr(),
+                                      V.data_ptr(), stream(s));
+    });
     return result(rc, std::move(q), std::move(k), std::move(v), std::move(K), std::move(V));
 }
 
@@ -175,8 +198,10 @@ PyObject* checkpoint_backward(const Ops* s, PyObject* const* a, Py_ssize_t n) {
     const void* dout = need(s, "dout", a[3], s->dtype, rows);
     at::Tensor dq = make(s, s->dtype, rows), dK = make(s, s->dtype, cache), dV = make(s, s->dtype, cache);
     at::Tensor dk = make(s, s->dtype, chunk), dv = make(s, s->dtype, chunk);
-    const int rc = h2o_checkpoint_backward(s->ctx, r.p, r.bytes, r.T, r.n, dout, dq.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-                                           dk.data_ptr(), dv.data_ptr(), stream(s));
+    const int rc = unlocked([&] {
+        return h2o_checkpoint_backward(s->ctx, r.p, r.bytes, r.T, r.n, dout, dq.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+                                       dk.data_ptr(), dv.data_ptr(), stream(s));
+    });
     return result(rc, std::move(dq), std::move(dK), std::move(dV), std::move(dk), std::move(dv));
 }
 
@@ -193,10 +218,13 @@ PyObject* carry_grad(const Ops* s, PyObject* const* a, Py_ssize_t nargs) {
     const void* gVn = a[7] == Py_None ? nullptr : need(s, "gV_next", a[7], at::kFloat, cache);
     at::Tensor gK = make(s, at::kFloat, cache), gV = make(s, at::kFloat, cache);
     at::Tensor gk = make(s, s->dtype, chunk), gv = make(s, s->dtype, chunk);
-    const int rc = h2o_carry_grad(s->ctx, static_cast<const int32_t*>(slots), narrow("token_slots", T), n, dK, dV, dk, dv,
-                                  static_cast<const float*>(gKn), static_cast<const float*>(gVn),
-                                  static_cast<float*>(gK.data_ptr()), static_cast<float*>(gV.data_ptr()), gk.data_ptr(),
-                                  gv.data_ptr(), stream(s));
+    const int t = narrow("token_slots", T);
+    const int rc = unlocked([&] {
+        return h2o_carry_grad(s->ctx, static_cast<const int32_t*>(slots), t, n, dK, dV, dk, dv,
+                              static_cast<const float*>(gKn), static_cast<const float*>(gVn),
+                              static_cast<float*>(gK.data_ptr()), static_cast<float*>(gV.data_ptr()), gk.data_ptr(),
+                              gv.data_ptr(), stream(s));
+    });
     return result(rc, std::move(gK), std::move(gV), std::move(gk), std::move(gv));
 }
 

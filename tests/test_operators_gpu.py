@@ -752,3 +752,64 @@ def test_backwards_of_growing_chunks_keep_few_workspaces():
     largest = 4 * B * (Hq + 2) * last * d + 16 * B * Hq * last + (32 << 20)  # the step, its statistics, parts and pages
     # grown to twice its size when outgrown: at most 2 + 1 + 1/2 + ... of the last one needed
     assert free - torch.cuda.mem_get_info()[0] <= 4 * largest
+
+
+def test_other_threads_run_while_a_call_waits():
+    """A context's first call waits for the work before it; Python's other threads do not."""
+    import threading
+    import time
+    q, k, v, K, V = heads(BF16, 1, 2, 2, 64, 64, 64, 8)
+    c, parent = cache_of(K, V, 4, 64), trees(1, 8)
+    torch.cuda.synchronize()
+    ticks, stop = [0], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks[0] += 1
+            time.sleep(1e-3)
+
+    t = threading.Thread(target=tick)
+    t.start()
+    try:
+        torch.cuda._sleep(int(8e8))  # 0.4 s at 2 GHz
+        before, start = ticks[0], time.monotonic()
+        c.tree_attend(q, k, v, parent)
+        passed, waited = ticks[0] - before, time.monotonic() - start
+    finally:
+        stop.set()
+        t.join()
+    assert waited > 0.1 and passed >= 10
+
+
+def test_two_threads_call_at_once():
+    """First calls of one context from two threads on one stream, its workspaces made and
+    outgrown meanwhile: what each call computes alone."""
+    import threading
+    inputs = [heads(BF16, 1, 2, 2, 64, 64, 64, T, seed=T) for T in (8, 40, 100, 200)]
+    K, V = inputs[0][3:]
+    alone = cache_of(K, V, 4, 64, max_T=8)
+    records = [alone.checkpoint(*x[:3]) for x in inputs]
+    douts, parents = [torch.randn_like(x[0]) for x in inputs], [trees(1, x[0].shape[2]) for x in inputs]
+
+    def run(c):
+        return [(c.checkpoint_backward(r, g), c.tree_attend(*x[:3], p)) for r, g, x, p in zip(records, douts, inputs, parents)]
+
+    want = run(alone)
+    for _ in range(5):
+        c, got = cache_of(K, V, 4, 64, max_T=8), [None, None]
+        go = threading.Barrier(2)
+
+        def work(i):
+            go.wait()
+            got[i] = run(c)
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        c.sync_check()
+        for both in got:
+            for mine, own in zip(both, want):
+                for a, b in zip(mine[0] + mine[1], own[0] + own[1]):
+                    assert torch.equal(a, b)
