@@ -23,8 +23,9 @@
 // pointer jumping (each round a node takes the mask of the node it points to and
 // points where that one does: 8 rounds for 256 nodes), by warps of their own while
 // the cache's blocks are worked on. Keys outside the mask get
-// weight zero; a drafted v with a NaN or an infinity is zeroed in shared memory,
-// because zero times it is not zero, and the rows that see it are set to NaN.
+// weight zero; a NaN or an infinity in a drafted v is zeroed in shared memory,
+// because zero times it is not zero, and at the end added to its column of the rows
+// that see it.
 // Rows past the end of a cache, of the nodes or of a KV head's queries arrive as
 // zeros (3-D tensor maps).
 //
@@ -66,7 +67,7 @@ struct TreeCfg {
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_MASK = OFF_RING + RING * TILE;                  // [256][8] words
     static constexpr int OFF_PTR = OFF_MASK + kTreeMaxT * kTreeMaskWords * 4;  // [256]
-    static constexpr int OFF_BAD = OFF_PTR + kTreeMaxT * 4;              // [2][4] words
+    static constexpr int OFF_BAD = OFF_PTR + kTreeMaxT * 4;                  // word
     static constexpr int OFF_MAX = OFF_BAD + 32;                             // [2 tiles][2 blocks][2 halves][128] floats
     static constexpr int OFF_BAR = OFF_MAX + 2 * 2 * 2 * 128 * 4;
     static constexpr int NBAR = 28;
@@ -99,6 +100,7 @@ struct TreeParams {
     Split split;        // of the blocks of all units
     float scale_log2;
     const int32_t* parent;
+    const __nv_bfloat16* v;  // of the nodes
     __nv_bfloat16* out;
     float* lse;
     float4* part_o;  // [2 CTAs][D / 4][256]: four columns of a row together, rows next to each other
@@ -226,11 +228,51 @@ __device__ __forceinline__ void merge_cluster(const TreeParams& p, const Segment
     }
 }
 
+// What is not finite in v of the nodes that a row sees, of a CTA's segments, added to the
+// row's output or part of it (weights are positive, so it is what the values' weighted
+// sum comes to). Rare: a CTA that met such a value does this once its outputs are
+// stored. `acc`: where a cluster's part lies.
+template <int D>
+__device__ __noinline__ void add_not_finite(const TreeParams& p, int w0, int w1, float* acc) {
+    for (int w = w0; w < w1;) {
+        const Segment s = segment(p, w, w0, w1);
+        w += s.j1 - s.j0;
+        const int lo = 128 * (s.j0 - p.nbc), hi = 128 * (s.j1 - p.nbc);  // its nodes
+        if (hi <= 0) continue;
+        const int32_t* parent = p.parent + (size_t)(s.bg / p.Hkv) * p.T;
+        for (int e = threadIdx.x; e < s.rows * D; e += TreeCfg<D>::THREADS) {
+            const int r = e / D, col = e % D;
+            float sum = 0.f;
+            bool any = false;
+            int u = (s.m0 + r) % p.T;
+            while (u >= 0) {
+                const float x = __bfloat162float(p.v[((size_t)s.bg * p.T + u) * D + col]);
+                if (u >= lo && u < hi && !isfinite(x)) {
+                    sum += x;
+                    any = true;
+                }
+                const int up = parent[u];
+                u = up == -1 ? -1 : (up >= 0 && up < u) ? up : -2;
+            }
+            if (!any || u != -1) continue;  // an absent node's row stays zero
+            if (p.cluster) {
+                acc[r * D + ((col / 4) ^ (r & (D / 4 - 1))) * 4 + col % 4] += sum;
+            } else if (s.whole) {
+                __nv_bfloat16* out = p.out + ((size_t)s.bg * p.R + s.m0 + r) * D + col;
+                *out = __float2bfloat16_rn(__bfloat162float(*out) + sum);
+            } else {
+                const size_t part = 2 * blockIdx.x + (s.first ? 0 : 1);
+                reinterpret_cast<float*>(p.part_o + (part * (D / 4) + col / 4) * kUnitRows + r)[col % 4] += sum;
+            }
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kc,
                const __grid_constant__ CUtensorMap map_vc, const __grid_constant__ CUtensorMap map_k,
-               const __grid_constant__ CUtensorMap map_v, const TreeParams p) {
+               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TreeParams p) {
     using Cfg = TreeCfg<D>;
     constexpr int RING = Cfg::RING;
     extern __shared__ uint8_t smem_raw[];
@@ -270,6 +312,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         mbar_init(mask_free, 16);
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAD) = 0;
         fence_mbar_init();
     }
     uint32_t tmem = 0;  // tile X: S at 256 X, O at 256 X + 128
@@ -469,7 +512,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t tS = tX + 64 * h, tO = tX + 128 + h * (D / 2);  // this thread's columns of S (and P) and O
         const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_MASK);
         const int* ptr = reinterpret_cast<const int*>(smem + Cfg::OFF_PTR);
-        uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAD);
         float* xmax = reinterpret_cast<float*>(smem + Cfg::OFF_MAX) + X * 512 + r;
         int L = 0, c = 0, tb = 0, done = 0, masks = 0;  // ring loads, blocks of this tile, node blocks, segments of this tile, with nodes
         bool ok = true;
@@ -487,14 +529,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const bool busy = s.m0 + 128 * X + 32 * quad < p.R;  // the warp has rows
             const int node = row % p.T;
             bool absent = false;
-            bool spoilt = false;  // the row sees a drafted v that is not finite
             float m = -INFINITY, l = 0.f;
             for (int j = s.j0; j < s.j1; ++j, ++c, L += 2) {
                 uint32_t vis[2] = {~0u, ~0u};  // of this thread's columns
                 const bool nodes = j >= p.nbc, masked = nodes || p.n - 128 * j < 128;
                 if (nodes && X == 0 && h == 0) {
-                    // V of the nodes: rows that are not finite become zeros
-                    uint32_t* bw = bad + 4 * (tb & 1);
+                    // V of the nodes: what is not finite becomes zero
                     const int slot = (L + 1) % RING;
                     if (ok) ok = warp_wait(ring_full + slot, ((L + 1) / RING) & 1, p.wb, kDevTimeoutTmaWait, abort_flag);
                     uint8_t* vt = smem + Cfg::OFF_RING + slot * Cfg::TILE + r * 128;
@@ -509,23 +549,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                     if (over) {
 #pragma unroll 1
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(vt + (x >> 3) * Cfg::HALF + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < D / 2; ++x) {
+                            uint32_t* u = reinterpret_cast<uint32_t*>(vt + (x >> 5) * Cfg::HALF) + (x & 31);
+                            if ((*u & 0x7f80u) == 0x7f80u) *u &= 0xffff0000u;
+                            if ((*u & 0x7f800000u) == 0x7f800000u) *u &= 0xffffu;
+                        }
+                        *reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_BAD) = 1;
                     }
-                    over = __ballot_sync(0xffffffffu, over != 0);
-                    if (lane == 0) bw[quad] = over;
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(v_ok + (tb & 1));
                 }
                 if (ok) ok = warp_wait(s_full + X, c & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
                 if (nodes) {
-                    if (ok) ok = warp_wait(v_ok + (tb & 1), (tb >> 1) & 1, p.wb, kDevTimeoutMmaWait, abort_flag);
                     if (ok) ok = warp_wait(mask_full, masks & 1, p.wb, kDevTimeoutSlotWait, abort_flag);
                     absent = ptr[node] != -1;
                     const uint32_t* mk = mask + node * kTreeMaskWords + 4 * (j - p.nbc);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) spoilt |= (mk[k] & bad[4 * (tb & 1) + k]) != 0;
                     vis[0] = mk[2 * h];
                     vis[1] = mk[2 * h + 1];
                     ++tb;
@@ -642,9 +681,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             const int chunk = (h * (D / 2) + x + e) / 4;
-                            uint4 w = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            if (spoilt) w.x = w.y = w.z = w.w = 0x7fffffffu;
-                            *reinterpret_cast<uint4*>(acc + (chunk ^ (r & (D / 4 - 1))) * 4) = w;
+                            *reinterpret_cast<uint4*>(acc + (chunk ^ (r & (D / 4 - 1))) * 4) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
                     if (h == 0)
@@ -665,7 +703,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     tc::reg_fence(o);
                     if (!row_ok) continue;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = spoilt ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * f);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                     const int col = h * (D / 2) + x;
                     if (!s.whole) {
                         float4* dst = p.part_o + (part * (D / 4) + col / 4) * kUnitRows + 128 * X + r;
@@ -690,31 +728,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
             }
             fence_before_sync();
-            if (p.count && !s.whole) {
-                // few rows: the unit's last CTA merges (one tile, so these are all 256
-                // threads), which spares a launch
-                __threadfence();
-                tc::named_sync(1 + X, 256);
-                unsigned* flag = reinterpret_cast<unsigned*>(smem + Cfg::OFF_MAX);
-                if (threadIdx.x == 64) {
-                    const unsigned before = atomicAdd(p.count + s.bg, 1u);
-                    *flag = before == (unsigned)p.split.k - 1;
-                    if (*flag) p.count[s.bg] = 0;
-                }
-                tc::named_sync(1 + X, 256);
-                if (*flag) {
-                    __threadfence();
-                    for (int e = threadIdx.x - 64; e < p.R * (D / 4); e += 256) merge_row<D>(p, s.bg, e % p.R, e / p.R);
-                }
-            }
         }
     }
     fence_before_sync();
+    __syncthreads();
+    if (*reinterpret_cast<const volatile uint32_t*>(smem + Cfg::OFF_BAD)) {
+        add_not_finite<D>(p, w0, w1, reinterpret_cast<float*>(smem + Cfg::OFF_RING));
+        __syncthreads();
+    }
     if (p.cluster) {
         __syncwarp();
         tc::cluster_sync();
-    } else {
-        __syncthreads();
     }
     if (warp == 1) {
         fence_after_sync();
@@ -723,6 +747,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (p.cluster) {
         merge_cluster<D>(p, segment(p, w0, w0, w1), sbase + Cfg::OFF_RING, sbase + Cfg::OFF_Q);
         tc::cluster_sync();  // no CTA leaves while another reads its part
+    } else if (p.count && w1 - w0 < p.nb) {
+        // few rows: the unit's last CTA merges, which spares a launch
+        const unsigned bg = w0 / p.nb;  // a unit per KV head
+        unsigned* flag = reinterpret_cast<unsigned*>(smem + Cfg::OFF_MAX);
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const unsigned before = atomicAdd(p.count + bg, 1u);
+            *flag = before == (unsigned)p.split.k - 1;
+            if (*flag) p.count[bg] = 0;
+        }
+        __syncthreads();
+        if (*flag) {
+            __threadfence();
+            for (int e = threadIdx.x; e < p.R * (D / 4); e += Cfg::THREADS) merge_row<D>(p, bg, e % p.R, e / p.R);
+        }
     }
 }
 
@@ -819,6 +859,7 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.split.extra = p.split.run % p.split.k;
     p.scale_log2 = kLog2e / sqrtf((float)D);
     p.parent = a.parent;
+    p.v = static_cast<const __nv_bfloat16*>(a.v);
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
     p.part_o = reinterpret_cast<float4*>(a.part);

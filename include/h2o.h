@@ -221,11 +221,10 @@ const char *h2o_last_error(const h2o_ctx *ctx);
  *   out [B, Hq, T, d]    softmax(q k / sqrt(d)) v,
  *   lse [B, Hq, T]       float: log-sum-exp of the row's scaled logits;
  * an absent node's row gets out = 0 and lse = -inf. A key that a row does not
- * see leaves the row alone whatever it holds (NaN and infinities included); a
- * row that sees a drafted node whose v holds a NaN or an infinity is NaN
- * throughout on the tensor-core path. Device pointers; layouts, element type
- * and alignment as h2o_step (parent and lse: 4 bytes); out and lse must not
- * overlap the inputs. T <= H2O_TREE_MAX_T
+ * see leaves the row alone whatever it holds (NaN and infinities included); in
+ * a drafted v that it does see, they reach the columns that hold them. Device
+ * pointers; layouts, element type and alignment as h2o_step (parent and lse: 4
+ * bytes); out and lse must not overlap the inputs. T <= H2O_TREE_MAX_T
  * (H2O_ERR_UNSUPPORTED otherwise, and under H2O_POLICY_INSERT_ALWAYS, where
  * the number of accepted tokens decides which slots a row may see). The scores
  * do not change: only committed tokens count. Asynchronous on `stream`. The

@@ -813,3 +813,51 @@ def test_two_threads_call_at_once():
             for mine, own in zip(both, want):
                 for a, b in zip(mine[0] + mine[1], own[0] + own[1]):
                     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d,n,T", [(FP32, 2, 2, 2, 64, 70, 12), (BF16, 2, 2, 4, 128, 700, 3), (BF16, 2, 2, 4, 128, 700, 40),
+                                                  (BF16, 2, 2, 2, 64, 130, 200), (BF16, 8, 8, 4, 128, 700, 3), (BF16, 14, 8, 4, 128, 300, 40),
+                                                  (BF16, 16, 4, 1, 64, 33, 256), (BF16, 14, 8, 4, 128, 2065, 40),
+                                                  (BF16, 1, 8, 4, 128, 8999, 3)])
+def test_tree_values_that_are_not_finite_stay_in_their_columns(dtype, B, Hkv, G, d, n, T):
+    """A NaN or an infinity in a drafted v is what the definition makes of it, whatever
+    the size of the call: in its column of the rows that see the node, and nowhere else."""
+    q, k, v, K, V = heads(dtype, B, Hkv, G, d, n, n, T, seed=5)
+    parent = trees(B, T, seed=6)
+    parent[:, :2] = torch.tensor([-1, 0])
+    want, wlse, bound, lbound = ref.tree(q, k, v, parent, K, V, n, dtype)
+    clean = cache_of(K, V, Hkv * G, n).tree_attend(q, k, v, parent)
+    bad = torch.zeros(v.shape, device="cuda")
+    bad[:, :, 0, 3], bad[:, :, 0, 17], bad[:, :, 0, d - 1] = math.nan, math.inf, -math.inf
+    bad[:, :, 1, 17], bad[:, :, 1, 40], bad[:, :, T - 1, d // 2] = -math.inf, math.inf, math.inf
+    bad[-1, -1, T // 2, 5] = -math.inf
+    out, lse = cache_of(K, V, Hkv * G, n).tree_attend(q, k, v + bad.to(dtype), parent)
+    see = ref.ancestors(parent).cuda()
+    extra = torch.zeros((B, Hkv, T, d), device="cuda")
+    for node in range(T):  # every weight is > 0: inf and NaN come through as they are
+        extra += torch.where(see[:, None, :, node, None], bad[:, :, None, node], 0.0)
+    extra = extra[:, :, None].expand(B, Hkv, G, T, d).reshape(out.shape)
+    there = extra.isfinite()
+    assert not there.all() and torch.equal(lse, clean[1])
+    assert torch.equal(out[~there].float().nan_to_num(nan=7.0), extra[~there].nan_to_num(nan=7.0))
+    # the finite columns: without the bad elements, whose own columns are not looked at
+    ref.within("out", out[there], want[there], bound[there])
+
+
+@pytest.mark.parametrize("B,T", [(1, 3), (2, 40), (14, 40), (16, 256)])
+def test_tree_values_that_are_not_finite_meet_others(B, T):
+    """Infinities of both signs in a slot and a node that share a column, and in rows
+    whose scores are NaN, give NaN on either path."""
+    q, k, v, K, V = heads(BF16, B, 4, 2, 64, 200, 200, T, seed=5)
+    parent = torch.zeros((B, T), dtype=torch.int32, device="cuda")
+    parent[:, 0] = -1
+    V[:, :, 7, 20] = math.inf
+    v[:, :, 0, 20], v[:, :, 0, 21], v[:, :, T - 1, 22] = -math.inf, math.inf, -math.inf
+    k[:, 1, 0, 3] = math.nan               # one KV head's rows are NaN
+    out, _ = cache_of(K, V, 8, 200).tree_attend(q, k, v, parent)
+    assert out[:, 2:4].isnan().all()
+    ok = out[:, [0, 1, 4, 5, 6, 7]]
+    assert ok[..., 20].isnan().all() and (ok[..., 21] == math.inf).all()
+    assert (ok[:, :, T - 1, 22] == -math.inf).all() and ok[:, :, :-1, 22].isfinite().all()
+    rest = [c for c in range(64) if c not in (20, 21, 22)]
+    assert ok[..., rest].isfinite().all()
