@@ -561,6 +561,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
     const int unit = cta / ranks;
     const int kb = unit / groups, bg = unit % groups;
     if (kb >= p.nbc + p.n_mblk) {
+        griddep_wait();  // who used dK and dV before is done with them
         const int s0 = 128 * (kb - p.n_mblk);
         const size_t at = ((size_t)bg * p.C + s0) * D;
         const int vecs = min(128, p.C - s0) * D / 8;
