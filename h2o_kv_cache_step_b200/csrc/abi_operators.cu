@@ -235,6 +235,8 @@ int h2o_checkpoint_backward(h2o_ctx* c, const void* ckpt, size_t bytes, int T, i
         return fail(c, H2O_ERR_ARG, "every pointer argument must be non-NULL");
     for (const void* p : {dout, (const void*)dq, (const void*)dK, (const void*)dV, (const void*)dk, (const void*)dv})
         if (!aligned16(p)) return fail(c, H2O_ERR_ALIGN, "every pointer argument must be 16-byte aligned");
+    if (c->dtype == H2O_BF16 && !c->use_tc)
+        return fail(c, H2O_ERR_UNSUPPORTED, "the bf16 backward runs on the tensor cores, which need the driver's tensor maps");
     DeviceGuard g(c->device);
     cudaStream_t s = (cudaStream_t)stream;
     CkptBwdArgs a{};

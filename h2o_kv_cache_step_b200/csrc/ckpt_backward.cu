@@ -44,11 +44,12 @@ __device__ __forceinline__ float4 sum_subs(float4 a) {
 // statistics. One pass over the keys with a running maximum, keeping
 // A = sum e dp k, Z = sum e k, sum e dp and sum e (e = exp(s - max)):
 // dq = (A - D Z) / (sum e sqrt(d)). Eight lanes share a key.
-template <typename E, int D, int kRows>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kWarps * 32, kRows * D <= 128 ? 2 : 1)
-ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
-                    const E* __restrict__ V, const E* __restrict__ dout, E* __restrict__ dq, float4* __restrict__ stats,
-                    int G, int T, int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+ckpt_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                    const float* __restrict__ K, const float* __restrict__ V, const float* __restrict__ dout,
+                    float* __restrict__ dq, float4* __restrict__ stats, int G, int T, int n, int pitch,
+                    int blocks_per_group, float scale_log2, float scale) {
     griddep_wait();  // the restored values are there
     griddep_launch_dependents();
     constexpr int Q4 = D / 32;
@@ -84,7 +85,7 @@ ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* _
         for (int b = 0; b < kBatch; ++b) {
             const int u = min(u0 + kStride * b + sub, total - 1);
             const size_t at = u < n ? (bg * pitch + u) * D : (bg * T + (u - n)) * D;
-            const E *kp = (u < n ? K : k) + at, *vp = (u < n ? V : v) + at;
+            const float *kp = (u < n ? K : k) + at, *vp = (u < n ? V : v) + at;
 #pragma unroll
             for (int c = 0; c < Q4; ++c) kk[b][c] = load4(kp + 32 * c + 4 * l8);
 #pragma unroll
@@ -180,12 +181,13 @@ ckpt_dq_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* _
 // dk and dv of kKeys keys of one KV group: key u < C is cache slot u (zero
 // gradients from n on), u >= C is chunk token u - C. Eight lanes share a query
 // row, the CTA takes 32 rows at a time.
-template <typename E, int D, int kKeys>
+template <int D, int kKeys>
 __global__ void __launch_bounds__(kWarps * 32, D == 64 ? 2 : 1)
-ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ K,
-                      const E* __restrict__ V, const E* __restrict__ dout, const float4* __restrict__ stats,
-                      E* __restrict__ dK, E* __restrict__ dV, E* __restrict__ dk, E* __restrict__ dv, int G, int C, int T,
-                      int n, int pitch, int blocks_per_group, float scale_log2, float scale) {
+ckpt_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                      const float* __restrict__ K, const float* __restrict__ V, const float* __restrict__ dout,
+                      const float4* __restrict__ stats, float* __restrict__ dK, float* __restrict__ dV,
+                      float* __restrict__ dk, float* __restrict__ dv, int G, int C, int T, int n, int pitch,
+                      int blocks_per_group, float scale_log2, float scale) {
     griddep_wait();  // the statistics are there
     constexpr int Q4 = D / 32;
     constexpr int kBatch = kKeys * D > 64 ? 2 : 4;
@@ -203,8 +205,8 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
         const bool cache = u < C;
         from[j] = cache ? (u < n ? 0 : T) : (u < C + T ? u - C : T);
         first = min(first, from[j]);
-        const E* kp = cache ? K + (bg * pitch + u) * D : k + (bg * T + (u - C)) * D;
-        const E* vp = cache ? V + (bg * pitch + u) * D : v + (bg * T + (u - C)) * D;
+        const float* kp = cache ? K + (bg * pitch + u) * D : k + (bg * T + (u - C)) * D;
+        const float* vp = cache ? V + (bg * pitch + u) * D : v + (bg * T + (u - C)) * D;
 #pragma unroll
         for (int c = 0; c < Q4; ++c) {
             const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -270,44 +272,44 @@ ckpt_dkdv_simt_kernel(const E* __restrict__ q, const E* __restrict__ k, const E*
             a = add4(a, part[0][i][j][x]);
             b = add4(b, part[1][i][j][x]);
         }
-        E* ka = u < C ? dK + (bg * C + u) * D : dk + (bg * T + (u - C)) * D;
-        E* va = u < C ? dV + (bg * C + u) * D : dv + (bg * T + (u - C)) * D;
+        float* ka = u < C ? dK + (bg * C + u) * D : dk + (bg * T + (u - C)) * D;
+        float* va = u < C ? dV + (bg * C + u) * D : dv + (bg * T + (u - C)) * D;
         store4(ka + 4 * x, scale4(a, scale));
         store4(va + 4 * x, b);
     }
 }
 
-template <typename E, int D, int kRows>
+template <int D, int kRows>
 cudaError_t dq_launch(const CkptBwdArgs& a, float scale) {
     const int G = a.Hq / a.Hkv, per = (G * a.T + kRows - 1) / kRows;
-    return launch_ex(true, ckpt_dq_simt_kernel<E, D, kRows>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
-                     a.stream, (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
-                     (E*)a.dq, reinterpret_cast<float4*>(a.stats), G, a.T, a.n, a.pitch, per, kLog2e * scale, scale);
+    return launch_ex(true, ckpt_dq_simt_kernel<D, kRows>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
+                     a.stream, (const float*)a.q, (const float*)a.k, (const float*)a.v, (const float*)a.K,
+                     (const float*)a.V, (const float*)a.dout, (float*)a.dq, reinterpret_cast<float4*>(a.stats), G, a.T,
+                     a.n, a.pitch, per, kLog2e * scale, scale);
 }
 
-template <typename E, int D, int kKeys>
+template <int D, int kKeys>
 cudaError_t dkdv_launch(const CkptBwdArgs& a, float scale) {
     const int G = a.Hq / a.Hkv, per = (a.C + a.T + kKeys - 1) / kKeys;
-    return launch_ex(true, ckpt_dkdv_simt_kernel<E, D, kKeys>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
-                     a.stream, (const E*)a.q, (const E*)a.k, (const E*)a.v, (const E*)a.K, (const E*)a.V, (const E*)a.dout,
-                     reinterpret_cast<const float4*>(a.stats), (E*)a.dK, (E*)a.dV, (E*)a.dk, (E*)a.dv, G, a.C, a.T, a.n,
-                     a.pitch, per, kLog2e * scale, scale);
+    return launch_ex(true, ckpt_dkdv_simt_kernel<D, kKeys>, dim3((unsigned)(a.B * a.Hkv * per)), dim3(kWarps * 32), 0,
+                     a.stream, (const float*)a.q, (const float*)a.k, (const float*)a.v, (const float*)a.K,
+                     (const float*)a.V, (const float*)a.dout, reinterpret_cast<const float4*>(a.stats), (float*)a.dK,
+                     (float*)a.dV, (float*)a.dk, (float*)a.dv, G, a.C, a.T, a.n, a.pitch, per, kLog2e * scale, scale);
 }
 
-template <typename E, int D>
-cudaError_t backward_typed(const CkptBwdArgs& a) {
+template <int D>
+cudaError_t backward_width(const CkptBwdArgs& a) {
     const float scale = 1.f / sqrtf((float)D);
     const long long ctas = 4ll * a.num_sms;
-    const cudaError_t e = (long long)a.B * a.Hq * a.T >= ctas ? dq_launch<E, D, 2>(a, scale) : dq_launch<E, D, 1>(a, scale);
+    const cudaError_t e = (long long)a.B * a.Hq * a.T >= ctas ? dq_launch<D, 2>(a, scale) : dq_launch<D, 1>(a, scale);
     if (e != cudaSuccess) return e;
-    return (long long)a.B * a.Hkv * (a.C + a.T) >= ctas ? dkdv_launch<E, D, 2>(a, scale) : dkdv_launch<E, D, 1>(a, scale);
+    return (long long)a.B * a.Hkv * (a.C + a.T) >= ctas ? dkdv_launch<D, 2>(a, scale) : dkdv_launch<D, 1>(a, scale);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a) {
-    if (a.dtype == 1) return a.d == 64 ? backward_typed<float, 64>(a) : backward_typed<float, 128>(a);
-    return a.d == 64 ? backward_typed<__nv_bfloat16, 64>(a) : backward_typed<__nv_bfloat16, 128>(a);
+    return a.d == 64 ? backward_width<64>(a) : backward_width<128>(a);
 }
 
 }  // namespace h2o

@@ -101,7 +101,7 @@ struct CkptBwdArgs {
 // parts of divided query tiles); needs the sizes and num_sms of a, enough for any
 // smaller T and n.
 size_t ckpt_stats_floats(const CkptBwdArgs& a);
-cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a);
+cudaError_t launch_ckpt_backward_simt(const CkptBwdArgs& a);  // fp32
 cudaError_t launch_ckpt_backward_tc(const CkptBwdArgs& a);  // bf16
 
 // Gradient of the cache after a step handed back through the eviction.
