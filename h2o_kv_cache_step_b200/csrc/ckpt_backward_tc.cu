@@ -12,31 +12,38 @@
 // ckpt_grad_tc_kernel   two kinds of CTA in one grid:
 //     dQ, one CTA per query tile: the two products again, dS = P (dP - D) over S in
 //     TMEM as a bf16 pair hi + lo, and dQ += hi K + lo K with them as A operands from
-//     TMEM: the terms of dq cancel (sum_j ds_j = 0, and keys have much in common), so
-//     8 bits of dS would cost it 1.7 times the rounding of the result (in 2-norm,
-//     heavy-hitter keys; dk and dv, whose terms cancel less, 1.4 times with one bf16
-//     each). The second product is 18 us of 121 at T=1024 C=2048.
+//     TMEM.
 //     dK and dV, one CTA, or a cluster, per (KV head, 128-key block), one key per TMEM
 //     lane: per query tile of the KV head, S^T = K Q^T and dP^T = V dO^T; P^T and dS^T
-//     go back over them as bf16 and are the A operands of dV += P^T dO and
+//     go back over them as bf16 pairs and are the A operands of dV += P^T dO and
 //     dK += dS^T Q.
+// With pairs (16 bits) a gradient's error is that of its own rounding to bf16, whatever
+// the size of the step. With one bf16 per weight it is, in 2-norm over heavy-hitter keys,
+// 1.7 times that for dq, whose terms cancel (sum_j ds_j = 0, and keys have much in
+// common), and 1.2 to 1.7 times for dk and dv. The second products of dq cost 18 us of
+// 121 at T=1024 C=2048, those of dk and dv 216 against 200 us a pass with the inputs in
+// L2 and 251 against 226 without.
 // Where query tiles are few, their key blocks are divided among several CTAs: the last
 // one of a tile adds up the statistics, and ckpt_dq_combine_kernel the parts of dQ, in
 // order.
 //
 // Bound by the tensor core: 2 products of 2 d per visible (row, key) for the
-// statistics, 4 for dQ and 4 for dK and dV. An operand pair from shared memory needs
-// 128 bytes a clock at the MMA's full rate, all there is, so P and dS stay in
-// TMEM (64 bytes a clock), and they never cross shared memory. A TMA loader, an MMA
+// statistics, 4 for dQ and 6 for dK and dV, a pair's two one after the other over the
+// same operand (all hi before all lo: 225 us a pass for 216). An operand pair from shared
+// memory needs 128 bytes a clock at the MMA's full rate, all there is, so P and dS stay
+// in TMEM (64 bytes a clock), and they never cross shared memory. A TMA loader, an MMA
 // issuer and four warpgroups that share every tile, 32 of its columns each (two with
 // 64: 202 us a pass at T=1024 C=2048 d=128 and 49 at B=2 T=333 C=1000 d=64; four: 197
-// and 47). The issue order keeps the tensor core on a product that
-// does not wait for the exponentials in progress: dV(t), S(t+1) while dS(t) is
-// computed, dK(t), dP(t+1) while P(t+1) is.
+// and 47; one bf16 per weight of dk and dv). The issue order keeps the tensor core on a
+// product that does not wait for the exponentials in progress: dV(t), S(t+1) while dS(t)
+// is computed, dK(t), dP(t+1) while P(t+1) is.
+//
+// Times of a pass are taken with the inputs in L2 and the clock not yet held down by
+// power, unless they say otherwise; with inputs that change from pass to pass
+// T=1024 C=2048 takes 251 us where it takes 216 so.
 //
 // Rows past the end of a KV head or cache arrive as zeros (3-D tensor maps), so
-// nothing of another head enters a tile. The MMA's operands are bf16; statistics
-// and gradients accumulate in fp32.
+// nothing of another head enters a tile. Statistics and gradients accumulate in fp32.
 #include <cuda.h>
 #include <math.h>
 
@@ -69,7 +76,6 @@ struct CkptTcParams {
     int nbC;     // 128-slot blocks of the whole cache
     int parts;   // CTAs per query tile, in both passes
     int dkdv_ctas, dq_ctas;  // of the gradients' grid
-    bool pairs;  // P and dS of dV and dK as bf16 pairs hi + lo, too
     float scale_log2, scale;
     float* nL2;     // [B*Hkv][128 * tiles]: -(log2-domain LSE) per row, -inf in padding rows
     float* D;       // [B*Hkv][128 * tiles], 0 in padding rows
@@ -660,14 +666,11 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
         };
         auto issue_ts = [&](uint32_t acc, uint32_t a, uint64_t b, bool first) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 rows at a time; every 32 rows at their columns
-                tc::mma_bf16_ts_warp(acc, a + 32 * (kk >> 1) + 8 * (kk & 1), b + (uint64_t)((kk * 16 * 128) >> 4),
-                                     Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
-            if (p.pairs) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_bf16_ts_warp(acc, a + 16 + 32 * (kk >> 1) + 8 * (kk & 1), b + (uint64_t)((kk * 16 * 128) >> 4),
-                                         Cfg::IDESC_G, 1u);
+            for (int kk = 0; kk < 8; ++kk) {  // 16 rows at a time; every 32 rows at their columns, hi and lo
+                const uint32_t ak = a + 32 * (kk >> 1) + 8 * (kk & 1);
+                const uint64_t bk = b + (uint64_t)((kk * 16 * 128) >> 4);
+                tc::mma_bf16_ts_warp(acc, ak, bk, Cfg::IDESC_G, (!first || kk > 0) ? 1u : 0u);
+                tc::mma_bf16_ts_warp(acc, ak + 16, bk, Cfg::IDESC_G, 1u);
             }
         };
         constexpr uint64_t kStage = (2 * Cfg::TILE) >> 4, kDO = Cfg::TILE >> 4;
@@ -757,7 +760,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
                 pk[(e >> 1) + 1] = tc::pack_bf16(pb.x, pb.y);
             }
             tc::tmem_st16(tl, pk);
-            if (p.pairs) store_rest(tl + 16, s, pk);
+            store_rest(tl + 16, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -779,7 +782,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& map_q, const CUtenso
                 pk[(e >> 1) + 1] = tc::pack_bf16(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
             }
             tc::tmem_st16(tl + 128, pk);
-            if (p.pairs) store_rest(tl + 144, s, pk);
+            store_rest(tl + 144, s, pk);
             tc::tmem_st_wait();
             fence_before_sync();
             __syncwarp();
@@ -853,8 +856,8 @@ ckpt_stats_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 // The gradients: dK and dV by the first CTAs, dQ by the rest, in one grid, so that
 // each fills the SMs the other leaves idle (one after the other, with the first pass
 // inside dQ's kernel: 242 us a pass at T=1024 C=2048 d=128 and 55 at B=2 T=333 C=1000
-// d=64, against 202 and 52). The longer CTAs, dK and dV's, go first (the other way
-// round: 218 us).
+// d=64, against 202 and 52, one bf16 per weight of dk and dv). The longer CTAs, dK and
+// dV's, go first (the other way round: 218 us).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 ckpt_grad_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
@@ -873,9 +876,10 @@ ckpt_grad_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 // key block, and a key block of a query tile, take about as long): the longest CTA if
 // all fit at once, else what an SM has to do, half of the longest CTA as the
 // unevenness of the last round, and kCtaTiles for what every CTA does besides.
-// Measured, clusters of 1, 2, 3 and 4: 202, 218, 247, 261 us a pass at T=1024 C=2048
-// d=128 (192 blocks of up to 32 tiles); 69, 53, 55, 54 at B=2 T=333 C=1000 d=64 (40
-// blocks of 21).
+// Measured, clusters of 1, 2, 3 and 4: 216, 230, 261, 276 us a pass at T=1024 C=2048
+// d=128 (192 blocks of up to 32 tiles), 104, 122, 142, 149 at T=512, 59, 62, 74, 84 at
+// T=384 C=1024; 68, 46, 52, 53 with changing inputs at B=2 T=333 C=1000 d=64, eight query
+// heads to a KV head (40 blocks of 21).
 int cluster_for(int groups, int tiles, int n_mblk, int nbc, int parts, int num_sms) {
     constexpr double kCtaTiles = 6.0;
     const double sum = 2.0 * groups * tiles * (nbc + 0.5 * (n_mblk + 1));
@@ -946,14 +950,6 @@ cudaError_t backward_launch(const CkptBwdArgs& a) {
     const int ranks = cluster_for((int)groups, p.tiles, p.n_mblk, p.nbc, p.parts, a.num_sms);
     p.dkdv_ctas = (int)((p.nbC + p.n_mblk) * groups * ranks);
     p.dq_ctas = (int)(p.tiles * groups * p.parts);
-    // dV and dK from bf16 pairs where that costs little: a small step waits for
-    // latencies, and its gradients are sums of fewer weights, whose roundings average
-    // out less (error against 64 bits, in roundings of the result: 1.2 to 1.7 with one
-    // bf16 each, 1.0 with pairs; large steps 1.4 with one). Measured, with pairs and
-    // without: 51.4 and 51.5 us a pass at B=2 T=333 C=1000 d=64 (5 products of a tile
-    // and a block per SM), 228 and 203 at T=1024 C=2048 d=128 (35 per SM).
-    constexpr int kPairWork = 16;
-    p.pairs = (long long)groups * p.tiles * (p.nbc + (p.n_mblk + 1) / 2) <= (long long)kPairWork * a.num_sms;
     cudaError_t e = launch_ex(true, ckpt_stats_tc_kernel<D>, dim3((unsigned)p.dq_ctas), dim3(kThreads), DqCfg<D>::SMEM, a.stream,
                               mq, mdo, mkc, mvc, mk, mv, p);
     if (e != cudaSuccess) return e;

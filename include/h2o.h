@@ -281,14 +281,15 @@ int h2o_checkpoint_restore(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, 
  *   dq [B,Hq,T,d], dK, dV [B,Hkv,C,d] (zero in the slots n..C-1),
  *   dk, dv [B,Hkv,T,d]
  * in the element type, each an fp32 sum rounded once, summed over the query
- * heads of a KV head. Rounding the record's values carries no gradient
- * (straight-through). NaNs and infinities in the record or in dout spoil the
- * gradients of their KV head. Device pointers, 16-byte aligned. The first call
- * (and one with T above the context's max_T and every T before) allocates a
- * workspace, which doubles at least when it is outgrown; the old one is kept
- * until the context goes. A call captured into a graph needs one of its size
- * before it. The workspace belongs to the context: its calls and replays must
- * not overlap on the GPU. Asynchronous on `stream`. */
+ * heads of a KV head (bf16: weights enter as pairs of bf16, 16 bits). Rounding
+ * the record's values carries no gradient (straight-through). NaNs and
+ * infinities in the record or in dout spoil the gradients of their KV head.
+ * Device pointers, 16-byte aligned. The first call (and one with T above the
+ * context's max_T and every T before) allocates a workspace, which doubles at
+ * least when it is outgrown; the old one is kept until the context goes. A call
+ * captured into a graph needs one of its size before it. The workspace belongs
+ * to the context: its calls and replays must not overlap on the GPU.
+ * Asynchronous on `stream`. */
 int h2o_checkpoint_backward(h2o_ctx *ctx, const void *ckpt, size_t bytes, int T, int n,
                             const void *dout, void *dq, void *dK, void *dV, void *dk, void *dv,
                             void *stream);
