@@ -23,9 +23,13 @@ constexpr int kWarps = 8, kStride = kWarps * 4;  // keys or rows of a CTA at a t
 // dq: query rows per CTA, and dk, dv: keys per CTA, in registers: two where that still
 // gives every SM two CTAs, one otherwise (64 rows, 320 keys, 4 / 2 heads: dq 9.6 us with
 // two and 8.0 with one, dk and dv 6.3 and 8.1). A lane group then has two or four keys
-// (rows) in flight: bound by the latency of its loads in small steps, by the fp32
-// pipe in large ones (one at a time, and so: 15.4 and 14.2 us a pass at 64 rows, 256
+// (rows) in flight (one at a time, and so: 15.4 and 14.2 us a pass at 64 rows, 256
 // slots, 4 / 2 heads, d = 64; 2748 and 2120 at 256 rows, 2048 slots, 32 / 8 heads, d = 128).
+// Bound by latencies, of loads from L2 and of the three exchanges that close a dot
+// product: in large steps the registers leave two warps to a scheduler, which issue in 46
+// (dq) and 40 % (dk, dv) of the cycles, and the fp32 pipe is busy in 33 and 24 % (64
+// rows, 1024 slots, 32 / 8 heads, d = 128: 160 and 192 us, where the eight products of d
+// per pair would take 59 at the pipe's full rate).
 
 __device__ __forceinline__ float sum8(float x) {  // over the eight lanes of a key or row
     x += __shfl_xor_sync(0xffffffffu, x, 1);

@@ -29,8 +29,15 @@
 // Rows past the end of a cache, of the nodes or of a KV head's queries arrive as
 // zeros (3-D tensor maps).
 //
-// P is rounded to bf16, the MMA's operand type; maxima, sums and outputs stay in
-// fp32 until the end.
+// P is rounded to bf16, the MMA's operand type, as in the step that commits the accepted
+// path and whose rows these are compared with; maxima, sums and outputs stay in fp32
+// until the end. The output's error against 64 bits is then 1.4 times that of its own
+// rounding. P as a bf16 pair makes it 1.0, for one more product per tile and block, which
+// the tensor core has no room for: 37.9 us a pass at T=61 B=4 C=4096 and 108 at T=256
+// C=16384, against 32.7 and 87.5.
+//
+// Times of a pass are taken with inputs that change from pass to pass, others with the
+// inputs in L2 and the clock not yet held down by power (T=256 C=16384: 86.6 and 81.8).
 #include <cuda.h>
 #include <math.h>
 
@@ -376,7 +383,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // QK(j + 1) together and then the other's: the two stay out of step, one in its
         // softmax while the other has the tensor core. With an issuer per tile their
         // products interleave, both wait and then both take exponentials (98 us at 256
-        // nodes and 16384 slots, against 83).
+        // nodes and 16384 slots, against 83 then).
         const uint64_t dQ = desc_kmajor_sw128(sbase + Cfg::OFF_Q);
         const uint64_t dRingK = desc_kmajor_sw128(sbase + Cfg::OFF_RING);
         const uint64_t dRingV = desc_mnmajor_sw128(sbase + Cfg::OFF_RING, Cfg::HALF);
@@ -834,8 +841,10 @@ cudaError_t tree_launch(const TreeArgs& a) {
     // fewer CTAs may work, but each leaves one part where most leave two; or among a
     // cluster, whose CTAs merge their parts in shared memory. A part that goes through
     // memory costs about as much as kPartBlocks blocks (its stores, and the merge of it).
-    // Measured, evenly, by unit, by clusters: 43.0, 36.4 and 31.6 us a pass at T=61 B=4
-    // C=4096; 85.3, 88.0 and 81.7 at T=256 C=16384.
+    // Measured, evenly, by unit, by clusters, 32 / 8 heads, d = 128 unless given: 41.2,
+    // 37.1 and 32.7 us a pass at T=61 B=4 C=4096; 91.4, 91.0 and 86.6 at T=256 C=16384.
+    // With inputs in L2: 28.6, 24.5 and 22.7 at T=100 B=2 C=2048; 40.4, 30.6 and 30.6 at
+    // T=256 C=8192, 16 / 4 heads; 44.1, 40.1 and 40.2 at T=128 C=16384, d = 64.
     constexpr int kPartBlocks = 2;
     const int units = (int)(total / p.nb), most = std::min(a.num_sms / units, p.nb);
     int k = 0, cost = (int)((total + a.num_sms - 1) / a.num_sms) + 2 * kPartBlocks;  // 0: evenly
@@ -865,8 +874,11 @@ cudaError_t tree_launch(const TreeArgs& a) {
     p.part_o = reinterpret_cast<float4*>(a.part);
     p.part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * a.num_sms * kUnitRows * D);
     p.wb = a.wb;
-    // Up to kMergeRows rows per KV head are merged by the unit's last CTA: measured,
-    // one token over 2048 slots, 14.4 us a pass against 15.4 with a kernel.
+    // Up to kMergeRows rows per KV head are merged by the unit's last CTA, where that is
+    // shorter than a kernel's launch. Measured, by the CTA and by a kernel, inputs in L2:
+    // 4 rows, C = 9000: 17.5 us and 18.0, C = 16384: 24.0 and 24.3; 8 rows, C = 9000: 17.4
+    // and 18.2; 32 rows, C = 16384: 26.2 to 30.4 and 25.3 to 30.0 (d = 64: 21.4 and 22.6);
+    // 48 rows: 31.6 and 27.5; 64 rows, d = 64: 24.3 and 23.6.
     constexpr int kMergeRows = 32;
     p.count = by_unit && R <= kMergeRows && !p.cluster ? a.count : nullptr;
     if (p.cluster) {

@@ -222,16 +222,18 @@ const char *h2o_last_error(const h2o_ctx *ctx);
  *   lse [B, Hq, T]       float: log-sum-exp of the row's scaled logits;
  * an absent node's row gets out = 0 and lse = -inf. A key that a row does not
  * see leaves the row alone whatever it holds (NaN and infinities included); in
- * a drafted v that it does see, they reach the columns that hold them. Device
- * pointers; layouts, element type and alignment as h2o_step (parent and lse: 4
- * bytes); out and lse must not overlap the inputs. T <= H2O_TREE_MAX_T
- * (H2O_ERR_UNSUPPORTED otherwise, and under H2O_POLICY_INSERT_ALWAYS, where
- * the number of accepted tokens decides which slots a row may see). The scores
- * do not change: only committed tokens count. Asynchronous on `stream`. The
- * first call allocates a workspace; a call captured into a graph needs one call
- * before it, and replays with the n of its capture. The workspace belongs to
- * the context: its calls and replays must not overlap on the GPU. The paper has
- * no counterpart of this entry point. */
+ * a drafted v that it does see, they reach the columns that hold them. In bf16
+ * the weights of larger calls are rounded to bf16 before they meet v, as the
+ * step's are. Device pointers; layouts, element type and alignment as h2o_step
+ * (parent and lse: 4 bytes); out and lse must not overlap the inputs. T <=
+ * H2O_TREE_MAX_T (H2O_ERR_UNSUPPORTED otherwise, and under
+ * H2O_POLICY_INSERT_ALWAYS, where the number of accepted tokens decides which
+ * slots a row may see). The scores do not change: only committed tokens count.
+ * Asynchronous on `stream`. The first call allocates a workspace; a call
+ * captured into a graph needs one call before it, and replays with the n of
+ * its capture. The workspace belongs to the context: its calls and replays
+ * must not overlap on the GPU. The paper has no counterpart of this entry
+ * point. */
 int h2o_tree_attend(h2o_ctx *ctx, const void *q, const void *k, const void *v,
                     const int32_t *parent, void *out, float *lse, int T, void *stream);
 
